@@ -1,0 +1,570 @@
+"""Cases of the operators around the microscaled 4-bit paged cache, and their plain forms.
+
+Three groups: "store" (quantise new keys and values into the pages of a cache, and read them back),
+"attend" (attention of one or a few queries of every sequence over such a cache) and "pages" (fork,
+extend, free, compact and copy the pages of the caches of several layers).
+
+With ``own`` false every case runs in elementary torch operations; with ``own`` true it makes the
+calls of the library. Rows of a batch are left-aligned: row t < counts[b] of sequence b belongs to
+position lens[b] - counts[b] + t of that sequence.
+"""
+import math
+import random
+
+import torch
+
+own = False
+
+_DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+_LEVELS = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+# ------------------------------------------------------------------------------ the cases
+def _store(name, B, Hkv, d, page, T, hist, dtype, fused, ragged, g=1.0):
+    return {"name": name, "kind": "store", "B": B, "Hkv": Hkv, "d": d, "page": page, "T": T, "hist": hist,
+            "dtype": dtype, "fused": fused, "ragged": ragged, "g": g}
+
+
+def _attend(name, B, Hkv, G, Lq, d, page, lo, hi, dtype, ragged, g=1.0):
+    return {"name": name, "kind": "attend", "B": B, "Hkv": Hkv, "G": G, "Lq": Lq, "d": d, "page": page,
+            "lo": lo, "hi": hi, "dtype": dtype, "ragged": ragged, "g": g}
+
+
+def _fork(name, parents, children, layers, Hkv, d, page, lo, hi):
+    return {"name": name, "kind": "fork", "parents": parents, "children": children, "layers": layers,
+            "Hkv": Hkv, "d": d, "page": page, "lo": lo, "hi": hi}
+
+
+def _churn(name, keep, short, late, layers, Hkv, d, page, lo, hi):
+    return {"name": name, "kind": "churn", "keep": keep, "short": short, "late": late, "layers": layers,
+            "Hkv": Hkv, "d": d, "page": page, "lo": lo, "hi": hi}
+
+
+def listed():
+    return [
+        # one decode step's new token for every sequence of a batch: the smallest write
+        _store("store_step", 16, 8, 128, 64, 1, 2000, "bf16", True, False),
+        # padded prompts of a batch, keys and values as views of the model's fused projection
+        _store("store_prompt", 8, 8, 128, 64, 4096, 0, "bf16", True, True),
+        # heads of 64 in fp16, small pages, an odd chunk appended behind a history
+        _store("store_heads64", 5, 12, 64, 16, 777, 411, "f16", False, True, 0.5),
+        # one short conversation: latency
+        _attend("attend_short", 1, 8, 4, 1, 128, 64, 333, 333, "bf16", False),
+        # a long-context decode step of a grouped-query model: the largest call
+        _attend("attend_32k", 16, 8, 4, 1, 128, 64, 32768, 32768, "bf16", False),
+        # many sequences with one query head per key head, heads of 64
+        _attend("attend_heads64", 64, 12, 1, 1, 64, 64, 8192, 8192, "f16", False),
+        # a serving batch of mixed lengths, eight query heads per key head, small pages
+        _attend("attend_ragged", 32, 8, 8, 1, 128, 16, 1, 16384, "bf16", True),
+        # drafts being verified: up to five queries a sequence, some with fewer
+        _attend("attend_draft", 8, 8, 4, 5, 128, 32, 700, 9001, "f16", True, 0.25),
+        # a few samples from one prompt
+        _fork("fork_samples", 1, 4, 1, 8, 128, 64, 1000, 1000),
+        # many samples a prompt, two layers' caches under one table
+        _fork("fork_beams", 24, 72, 2, 8, 128, 64, 700, 3500),
+        # a small server: requests come and go
+        _churn("churn_small", 4, 3, 3, 1, 8, 128, 64, 100, 900),
+        # a busy one: the live pages are packed after a wave of requests has left
+        _churn("churn_wave", 32, 48, 64, 2, 8, 128, 64, 300, 1500),
+    ]
+
+
+def _logint(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    kind = rng.choice(["store", "attend", "attend", "fork", "churn"])
+    d, page, g = rng.choice([64, 128, 128, 256]), rng.choice([16, 32, 64, 128]), rng.choice([0.25, 0.5, 1.0, 2.0])
+    Hkv = rng.choice([1, 2, 4, 8, 12])
+    if kind == "store":
+        B = _logint(rng, 1, 64)
+        T = _logint(rng, 1, max(1, min(4096, 2 ** 25 // (B * Hkv * d))))
+        c = _store("", B, Hkv, d, page, T, _logint(rng, 1, 3000) - 1, rng.choice(["bf16", "f16", "f32"]),
+                   rng.random() < 0.5, rng.random() < 0.5, g)
+    elif kind == "attend":
+        B, G, Lq = _logint(rng, 1, 64), rng.choice([1, 2, 3, 4, 5, 7, 8]), rng.choice([1, 1, 1, 2, 3, 4, 8, 16])
+        room = 2 ** 28 // (B * Hkv * d * ((G * Lq + 15) // 16))
+        hi = _logint(rng, 1, max(1, min(65536, room)))
+        c = _attend("", B, Hkv, G, Lq, d, page, _logint(rng, 1, hi), hi, rng.choice(["bf16", "f16"]),
+                    rng.random() < 0.7, g)
+    elif kind == "fork":
+        parents = _logint(rng, 1, 24)
+        hi = _logint(rng, 2, 3500)
+        c = _fork("", parents, _logint(rng, 1, 72), rng.choice([1, 2]), min(Hkv, 8), min(d, 128), page,
+                  _logint(rng, 1, hi), hi)
+    else:
+        hi = _logint(rng, 2, 1500)
+        c = _churn("", _logint(rng, 1, 32), _logint(rng, 1, 48), _logint(rng, 1, 64), rng.choice([1, 2]),
+                   min(Hkv, 8), min(d, 128), page, _logint(rng, 1, hi), hi)
+    del c["name"]
+    return c
+
+
+def _spread(lo, hi, n, salt):
+    """n lengths between lo and hi, spread over their logarithm, the same for every seed."""
+    r = random.Random(salt)
+    return [hi if lo == hi else _logint(r, lo, hi) for _ in range(n)]
+
+
+def _rows(c):
+    """(lengths, counts) of a store or attend case, on the host."""
+    n = c["T"] if c["kind"] == "store" else c["Lq"]
+    if c["kind"] == "store":
+        counts = _spread(1, n, c["B"], 3 * n + 1) if c["ragged"] else [n] * c["B"]
+        hist = _spread(1, c["hist"], c["B"], n) if c["hist"] else [0] * c["B"]
+        return [h + k for h, k in zip(hist, counts)], counts
+    lens = _spread(c["lo"], c["hi"], c["B"], c["hi"] + c["B"])
+    if c["ragged"] and c["B"] > 3:
+        lens[2], lens[-1] = 0, c["hi"]  # a slot of the batch that holds no sequence, and a full one
+    r = random.Random(n)
+    counts = [min(L, r.randint(1, n)) if c["ragged"] else min(L, n) for L in lens]
+    return lens, counts
+
+
+def _pages_of(lens, page):
+    return [(L + page - 1) // page for L in lens]
+
+
+# ------------------------------------------------------------------------------ inputs
+def _randn(gen, *shape):
+    return torch.randn(*shape, generator=gen, device="cuda", dtype=torch.float32)
+
+
+def _keys(gen, shape, d, seed):
+    """Keys with a few loud channels and norms that vary from token to token."""
+    x = _randn(gen, *shape, d)
+    loud = random.Random(seed).sample(range(d), 4)
+    x[..., loud] *= 20.0
+    return x.mul_(torch.rand(*shape, 1, generator=gen, device="cuda") * 1.5 + 0.5)
+
+
+def _table(npages, max_pages, gen, first=0, total=None):
+    """Pages of the sequences, scattered over total pages from `first` on; -1 where there is none."""
+    used = sum(npages)
+    total = used if total is None else total
+    perm = torch.randperm(total, generator=gen, device="cuda")[:used].to(torch.int32) + first
+    bt = torch.full((len(npages), max_pages), -1, dtype=torch.int32, device="cuda")
+    at = 0
+    for b, n in enumerate(npages):
+        bt[b, :n] = perm[at:at + n]
+        at += n
+    return bt
+
+
+def _ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def _library():
+    from quantized_decode_attention_kv_b200 import tq
+    return tq
+
+
+def prepare(case, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    if case["kind"] in ("fork", "churn"):
+        return _prepare_pages(case, gen)
+    B, Hkv, d, page, g = case["B"], case["Hkv"], case["d"], case["page"], case["g"]
+    lens, counts = _rows(case)
+    npages = _pages_of(lens, page)
+    max_pages = max(1, max(npages))
+    num_pages = sum(npages) + 7
+    st = {"case": case, "host_lens": lens, "host_counts": counts, "lens": _ints(lens), "counts": _ints(counts),
+          "table": _table(npages, max_pages, gen, 0, num_pages), "scale": d ** -0.5}
+    for side in "kv":
+        st[side + "_codes"] = torch.zeros(num_pages, Hkv, page, d // 2, dtype=torch.uint8, device="cuda")
+        st[side + "_scales"] = torch.zeros(num_pages, Hkv, page, d // 16, dtype=torch.uint8, device="cuda")
+    dt = _DT[case["dtype"]]
+    if case["kind"] == "store":
+        T = case["T"]
+        k = _keys(gen, (B, T, Hkv), d, seed).to(dt)
+        v = _randn(gen, B, T, Hkv, d).to(dt)
+        if case["fused"]:  # two slices of one [B, T, heads, d] projection, as a model produces them
+            x = torch.cat([k, v], dim=2)
+            st["K"], st["V"] = x[:, :, :Hkv].transpose(1, 2), x[:, :, Hkv:].transpose(1, 2)
+        else:
+            st["K"], st["V"] = k.transpose(1, 2).contiguous(), v.transpose(1, 2).contiguous()
+    else:
+        for b, L in enumerate(lens):
+            n = npages[b]
+            for side, x in (("k", _keys(gen, (n * page, Hkv), d, seed) if n else None),
+                            ("v", _randn(gen, n * page, Hkv, d) if n else None)):
+                if n:
+                    codes, scales = _quantise(x, g)
+                    at = st["table"][b, :n].long()
+                    st[side + "_codes"][at] = codes.view(n, page, Hkv, -1).transpose(1, 2)
+                    st[side + "_scales"][at] = scales.view(n, page, Hkv, -1).transpose(1, 2)
+        st["q"] = _randn(gen, B, case["Lq"], Hkv * case["G"], d).to(dt)
+    if own:
+        tq = _library()
+        cache = tq.TQMXCache(B, Hkv, d, page, num_pages, max_pages, st["table"], k_scale=g, v_scale=g)
+        for key in ("k_codes", "k_scales", "v_codes", "v_scales"):
+            cache[key].copy_(st.pop(key))
+        st["cache"] = cache
+        if case["kind"] == "store":
+            st["K_out"] = torch.empty(B, Hkv, case["T"], d, dtype=dt, device="cuda")
+            st["V_out"] = torch.empty_like(st["K_out"])
+        else:
+            st["out"] = torch.empty_like(st["q"])
+            st["ws"] = tq.workspace(tq.tq_decode_mx_workspace_bytes(cache, Hkv * case["G"], case["Lq"]))
+    return st
+
+
+def _prepare_pages(case, gen):
+    page, Hkv, d, layers = case["page"], case["Hkv"], case["d"], case["layers"]
+    st = {"case": case}
+    if case["kind"] == "fork":
+        parents, children = case["parents"], case["children"]
+        B = parents + children
+        lens = _spread(case["lo"], case["hi"], parents, 17) + [0] * children
+        npages = _pages_of(lens, page)
+        r = random.Random(5)
+        parent_of = [-1] * parents + [r.randrange(parents) for _ in range(children)]
+        need = [0] * parents + [r.randint(1, 2 * page) for _ in range(children)]
+        num_pages = sum(npages) + 4 * children + 9
+        st["table"] = _table(npages, max(npages) + 3, gen, 0, num_pages)
+        st["parent_of"], st["need"] = _ints(parent_of), _ints(need)
+        st["leaving"] = _ints([int(p >= 0) for p in parent_of])
+        held = []
+    else:
+        keep, short, late = case["keep"], case["short"], case["late"]
+        B = keep + short + late
+        full = _spread(case["lo"], case["hi"], B, 23)
+        lens = full[:keep] + [0] * (short + late)
+        npages = _pages_of(lens, page)
+        spare = max(1, sum(npages) // 8)  # pages held for snapshots of the kept sequences' pages
+        held = list(range(spare))
+        num_pages = spare + sum(_pages_of(full, page)) + 11
+        st["table"] = _table(npages, max(_pages_of(full, page)), gen, spare)
+        st["need_short"] = _ints([L if keep <= b < keep + short else 0 for b, L in enumerate(full)])
+        st["need_late"] = _ints([L if b >= keep + short else 0 for b, L in enumerate(full)])
+        st["is_short"] = _ints([int(keep <= b < keep + short) for b in range(B)])
+        st["is_late"] = _ints([int(b >= keep + short) for b in range(B)])
+        used = sum(npages)
+        st["copy_src"] = [spare + i * used // spare for i in range(spare)]
+        st["copy_dst"] = held
+        st["copy_src_dev"], st["copy_dst_dev"] = _ints(st["copy_src"]).long(), _ints(held).long()
+    refs = torch.zeros(num_pages, dtype=torch.int32, device="cuda")
+    refs[st["table"][st["table"] >= 0].long()] = 1
+    refs[held] = 1
+    st["refs"], st["lens"] = refs, _ints(lens)
+    st["status"] = torch.zeros(3, dtype=torch.int32, device="cuda")
+    st["live"] = torch.zeros(1, dtype=torch.int32, device="cuda")
+    st["pools"] = []
+    for _ in range(layers):
+        for _side in "kv":
+            for width in (d // 2, d // 16):
+                st["pools"].append(torch.randint(0, 256, (num_pages, Hkv, page, width), generator=gen,
+                                                 device="cuda", dtype=torch.uint8))
+    if own:
+        tq = _library()
+        pool = tq.TQPagePool(B, st["table"].shape[1], num_pages, page)
+        pool.block_table.copy_(st["table"])
+        pool.refs.copy_(refs)
+        pool.lens.copy_(st["lens"])
+        st["pool"] = pool
+        st["caches"] = []
+        for i in range(layers):
+            cache = tq.TQMXCache(B, Hkv, d, page, num_pages, st["table"].shape[1], pool.block_table)
+            for j, key in enumerate(("k_codes", "k_scales", "v_codes", "v_scales")):
+                cache[key].copy_(st["pools"][4 * i + j])
+                st["pools"][4 * i + j] = cache[key]
+            st["caches"].append(cache)
+        st["table"], st["refs"], st["lens"] = pool.block_table, pool.refs, pool.lens
+        st["arrays"] = tq.tq_page_arrays(st["caches"])
+        st["ws"] = tq.workspace(tq.tq_pages_workspace_bytes(pool))
+    return st
+
+
+# ------------------------------------------------------------------------------ plain forms
+def _quantise(x, g):
+    """[..., d] -> packed E2M1 codes [..., d/2] (even elements in the low half of a byte) and E4M3
+    scale bytes [..., d/16]."""
+    x = x.float()
+    blocks = x.reshape(*x.shape[:-1], x.shape[-1] // 16, 16)
+    top = blocks.abs().amax(dim=-1)
+    gf = torch.tensor(g, dtype=torch.float32, device=x.device)
+    stored = (top / (6.0 * gf)).clamp(max=448.0).to(torch.float8_e4m3fn)
+    step = (stored.float() * gf).unsqueeze(-1)
+    u = torch.where(step > 0, blocks / step, torch.zeros_like(blocks))
+    a = u.abs()
+    code = ((a > 0.25).to(torch.uint8) + (a >= 0.75).to(torch.uint8) + (a > 1.25).to(torch.uint8)
+            + (a >= 1.75).to(torch.uint8) + (a > 2.5).to(torch.uint8) + (a >= 3.5).to(torch.uint8)
+            + (a > 5.0).to(torch.uint8))
+    code = (code + 8 * (u < 0).to(torch.uint8)).reshape(x.shape)
+    return code[..., 0::2] | (code[..., 1::2] << 4), stored.view(torch.uint8)
+
+
+def _values(codes, scales, g):
+    """The 32-bit values of packed codes and their scales."""
+    table = torch.tensor(_LEVELS + tuple(-v for v in _LEVELS), dtype=torch.float32, device=codes.device)
+    pair = torch.stack([codes & 15, codes >> 4], dim=-1).reshape(*codes.shape[:-1], codes.shape[-1] * 2)
+    v = table[pair.int()].reshape(*scales.shape, 16) * scales.view(torch.float8_e4m3fn).float().unsqueeze(-1)
+    return v.reshape(pair.shape) * g
+
+
+def _plain_store(st):
+    c = st["case"]
+    page, T = c["page"], c["T"]
+    n = sum(st["host_counts"])
+    counts = st["counts"].long()
+    b = torch.repeat_interleave(torch.arange(c["B"], device="cuda"), counts, output_size=n)
+    t = torch.arange(n, device="cuda") - (counts.cumsum(0) - counts)[b]
+    pos = st["lens"].long()[b] - counts[b] + t
+    at, slot = st["table"][b, pos // page].long(), pos % page
+    outs = []
+    for side, x in (("k", st["K"]), ("v", st["V"])):
+        codes, scales = st[side + "_codes"], st[side + "_scales"]
+        codes[at, :, slot], scales[at, :, slot] = _quantise(x[b, :, t], c["g"])
+        out = torch.zeros(x.shape, dtype=x.dtype, device="cuda")
+        out[b, :, t] = _values(codes[at, :, slot], scales[at, :, slot], c["g"]).to(x.dtype)
+        outs.append(out)
+    return outs
+
+
+def _plain_attend(st):
+    c = st["case"]
+    page, Hkv, G, d = c["page"], c["Hkv"], c["G"], c["d"]
+    out = torch.zeros_like(st["q"])
+    for b, (L, n) in enumerate(zip(st["host_lens"], st["host_counts"])):
+        if L == 0 or n == 0:
+            continue
+        at = st["table"][b, :(L + page - 1) // page].long()
+        kv = []
+        for side in "kv":
+            codes = st[side + "_codes"][at].transpose(0, 1).reshape(Hkv, -1, d // 2)[:, :L]
+            scales = st[side + "_scales"][at].transpose(0, 1).reshape(Hkv, -1, d // 16)[:, :L]
+            kv.append(_values(codes, scales, c["g"]))
+        q = st["q"][b, :n].float().reshape(n, Hkv, G, d).permute(1, 2, 0, 3).reshape(Hkv, G * n, d)
+        s = torch.matmul(q, kv[0].transpose(1, 2)).reshape(Hkv, G, n, L) * st["scale"]
+        seen = torch.arange(L, device="cuda")[None, :] <= (L - n + torch.arange(n, device="cuda"))[:, None]
+        s = s.masked_fill(~seen, float("-inf"))
+        p = torch.exp(s - s.amax(dim=-1, keepdim=True))
+        p = p / p.sum(dim=-1, keepdim=True)
+        o = torch.matmul(p.reshape(Hkv, G * n, L), kv[1]).reshape(Hkv, G, n, d)
+        out[b, :n] = o.permute(2, 0, 1, 3).reshape(n, Hkv * G, d).to(out.dtype)
+    return out
+
+
+def _plain_free(st, leaving):
+    gone = leaving.bool()[:, None] & (st["table"] >= 0)
+    st["refs"].index_add_(0, st["table"].clamp(min=0).flatten(), -gone.flatten().int())
+    st["table"].masked_fill_(leaving.bool()[:, None], -1)
+    st["lens"].masked_fill_(leaving.bool(), 0)
+
+
+def _free_order(refs):
+    return torch.argsort((refs != 0).to(torch.uint8), stable=True).to(torch.int32)
+
+
+def _plain_extend(st, need, status):
+    page, table, refs, lens = st["case"]["page"], st["table"], st["refs"], st["lens"]
+    after = lens + need.clamp(min=0)
+    had, has = (lens + page - 1) // page, (after + page - 1) // page
+    add = has - had
+    fits = (has <= table.shape[1]).all()
+    enough = add.sum() <= (refs == 0).sum()
+    ok = fits & enough
+    status.copy_(torch.where(fits, torch.where(enough, 0, 1), 2))
+    j = torch.arange(table.shape[1], device="cuda")[None, :]
+    new = (j >= had[:, None]) & (j < has[:, None]) & ok
+    rank = (add.cumsum(0) - add - had)[:, None] + j
+    got = _free_order(refs)[rank.clamp(0, refs.numel() - 1)]
+    refs.index_add_(0, got.flatten(), new.flatten().int())
+    table.copy_(torch.where(new, got, table))
+    lens.copy_(torch.where(ok, after, lens))
+
+
+def _plain_fork(st, parent_of, status):
+    page, table, refs, lens = st["case"]["page"], st["table"], st["refs"], st["lens"]
+    me = torch.arange(table.shape[0], device="cuda")
+    valid = (parent_of >= 0) & (parent_of < table.shape[0]) & (parent_of != me)
+    src = torch.where(valid, parent_of, me).long()
+    length = lens[src]
+    partial = valid & (length % page != 0)
+    ok = partial.sum() <= (refs == 0).sum()
+    status.copy_(torch.where(ok, 0, 1))
+    valid, partial = valid & ok, partial & ok
+    fresh = _free_order(refs)[(partial.int().cumsum(0) - 1).clamp(min=0)]
+    last = (length - 1).clamp(min=0) // page
+    old = table.clone()
+    rows = old[src]
+    j = torch.arange(table.shape[1], device="cuda")[None, :]
+    rows = torch.where(j < ((length + page - 1) // page)[:, None], rows, -1)
+    tail = rows.gather(1, last[:, None].long()).squeeze(1)
+    rows = torch.where(partial[:, None] & (j == last[:, None]), fresh[:, None], rows)
+    rows = torch.where(valid[:, None], rows, old)
+    for entries, sign in ((old, -1), (rows, 1)):
+        held = valid[:, None] & (entries >= 0)
+        refs.index_add_(0, entries.clamp(min=0).flatten(), sign * held.flatten().int())
+    table.copy_(rows)
+    lens.copy_(torch.where(valid, length, lens))
+    which = partial.nonzero().squeeze(1)
+    for pool in st["pools"]:
+        pool[fresh[which].long()] = pool[tail[which].long()]
+
+
+def _plain_compact(st, live):
+    refs = st["refs"]
+    alive = refs != 0
+    n = alive.sum()
+    live.copy_(n)
+    index = torch.arange(refs.numel(), device="cuda")
+    src = (alive & (index >= n)).nonzero().squeeze(1).flip(0)
+    dst = (~alive & (index < n)).nonzero().squeeze(1)
+    for pool in st["pools"]:
+        pool[dst] = pool[src]
+    refs[dst] = refs[src]
+    refs[src] = 0
+    moved = torch.arange(refs.numel(), dtype=torch.int32, device="cuda")
+    moved[src] = dst.int()
+    st["table"].copy_(torch.where(st["table"] >= 0, moved[st["table"].clamp(min=0).long()], -1))
+
+
+def _plain_copy(st, src, dst):
+    for pool in st["pools"]:
+        pool[dst] = pool[src]
+
+
+# ------------------------------------------------------------------------------ one pass
+def run(state):
+    st, kind = state, state["case"]["kind"]
+    tq = _library() if own else None
+    if kind == "store":
+        if not own:
+            return _plain_store(st)
+        tq.tq_quantize_kv_mx(st["K"], st["V"], st["cache"], st["lens"], st["counts"])
+        tq.tq_dequantize_mx(st["cache"], st["lens"], st["K_out"], st["V_out"], st["counts"])
+        return [st["K_out"], st["V_out"]]
+    if kind == "attend":
+        if not own:
+            return _plain_attend(st)
+        tq.tq_decode_attention_mx(st["q"], st["cache"], st["lens"], st["scale"], st["out"], st["ws"], st["counts"])
+        return st["out"]
+    if kind == "fork":  # the children of the last pass leave, new ones are forked and get room to grow
+        if own:
+            tq.tq_pages_free(st["pool"], st["leaving"])
+            tq.tq_pages_fork(st["pool"], st["arrays"], st["parent_of"], st["status"][0:1], st["ws"])
+            tq.tq_pages_extend(st["pool"], st["need"], st["status"][1:2], st["ws"])
+        else:
+            _plain_free(st, st["leaving"])
+            _plain_fork(st, st["parent_of"], st["status"][0])
+            _plain_extend(st, st["need"], st["status"][1])
+    else:  # a wave of requests comes and goes, a later one stays: its pages are packed; then a snapshot
+        if own:
+            tq.tq_pages_free(st["pool"], st["is_late"])
+            tq.tq_pages_extend(st["pool"], st["need_short"], st["status"][0:1], st["ws"])
+            tq.tq_pages_extend(st["pool"], st["need_late"], st["status"][1:2], st["ws"])
+            tq.tq_pages_free(st["pool"], st["is_short"])
+            tq.tq_pages_compact(st["pool"], st["arrays"], st["live"], st["ws"])
+            tq.tq_pages_copy(st["arrays"], st["copy_src"], st["copy_dst"])
+        else:
+            _plain_free(st, st["is_late"])
+            _plain_extend(st, st["need_short"], st["status"][0])
+            _plain_extend(st, st["need_late"], st["status"][1])
+            _plain_free(st, st["is_short"])
+            _plain_compact(st, st["live"][0])
+            _plain_copy(st, st["copy_src_dev"], st["copy_dst_dev"])
+    return [st["table"], st["refs"], st["lens"], st["status"], st["live"]] + st["pools"]
+
+
+# ------------------------------------------------------------------------------ what a pass cannot do without
+def work(case):
+    c = case
+    if c["kind"] == "store":
+        rows = sum(_rows(c)[1]) * c["Hkv"] * 2
+        width = 4 if c["dtype"] == "f32" else 2
+        record = c["d"] // 2 + c["d"] // 16
+        padded = c["B"] * c["T"] * c["Hkv"] * 2 * c["d"] * width  # the rows read back, padding as zeros
+        return {"bytes": rows * (c["d"] * width + 2 * record) + padded, "flops": rows * c["d"] * 3}
+    if c["kind"] == "attend":
+        lens, counts = _rows(c)
+        record = c["d"] // 2 + c["d"] // 16
+        rows = c["B"] * c["Lq"] * c["Hkv"] * c["G"]
+        return {"bytes": sum(lens) * c["Hkv"] * 2 * record + rows * c["d"] * 4,
+                "flops": sum(L * n for L, n in zip(lens, counts)) * c["Hkv"] * c["G"] * 4 * c["d"]}
+    page_bytes = c["page"] * c["Hkv"] * 2 * (c["d"] // 2 + c["d"] // 16) * c["layers"]
+    page = c["page"]
+    if c["kind"] == "fork":
+        lens = _spread(c["lo"], c["hi"], c["parents"], 17)
+        r = random.Random(5)
+        of = [r.randrange(c["parents"]) for _ in range(c["children"])]
+        moved = sum(1 for p in of if lens[p] % page)
+        entries = sum(_pages_of([lens[p] for p in of], page))
+        return {"bytes": 2 * moved * page_bytes + entries * 16, "flops": 0}
+    full = _spread(c["lo"], c["hi"], c["keep"] + c["short"] + c["late"], 23)
+    kept = sum(_pages_of(full[:c["keep"]], page))
+    short = sum(_pages_of(full[c["keep"]:c["keep"] + c["short"]], page))
+    late = sum(_pages_of(full[c["keep"] + c["short"]:], page))
+    moved = min(short, late) + max(1, kept // 8)
+    return {"bytes": 2 * moved * page_bytes + (short + late) * 24, "flops": 0}
+
+
+# ------------------------------------------------------------------------------ from the definition, in 64 bits
+def _round_e4m3(v):
+    v = v.clamp(max=448.0)
+    _, e = torch.frexp(v)
+    unit = torch.ldexp(torch.ones_like(v), (e - 1).clamp(min=-6) - 3)
+    return torch.round(v / unit) * unit  # ties to even
+
+
+def _exact_store(st):
+    outs = []
+    c = st["case"]
+    rows = torch.arange(c["T"], device="cuda")[None, :] < st["counts"][:, None]
+    for x in (st["K"], st["V"]):
+        v = x.double().reshape(*x.shape[:-1], -1, 16)
+        step = _round_e4m3(v.abs().amax(-1, keepdim=True) / (6.0 * c["g"])) * c["g"]
+        u = torch.where(step > 0, v / torch.where(step > 0, step, 1.0), 0.0)
+        a = u.abs()
+        unit = torch.where(a < 2, 0.5, torch.where(a < 4, 1.0, 2.0)).double()
+        a = (torch.round(a / unit) * unit).clamp(max=6.0)
+        y = (torch.sign(u) * a * step).reshape(x.shape)
+        outs.append(torch.where(rows[:, None, :, None], y, 0.0))
+    return outs
+
+
+def _exact_values(codes, scales, g):
+    e = (scales >> 3).double()
+    m = (scales & 7).double()
+    s = torch.where(e > 0, (1 + m / 8) * torch.exp2(e - 7), m * 2.0 ** -9)
+    out = torch.empty(*codes.shape, 2, dtype=torch.float64, device=codes.device)
+    for half, nib in enumerate((codes % 16, codes // 16)):
+        ee, mm = ((nib // 2) % 4).double(), (nib % 2).double()
+        mag = torch.where(ee > 0, (1 + mm / 2) * torch.exp2(ee - 1), mm / 2)
+        out[..., half] = torch.where(nib >= 8, -mag, mag)
+    out = out.flatten(-2)
+    return (out.reshape(*scales.shape, 16) * (s * g)[..., None]).reshape(out.shape)
+
+
+def _exact_attend(st):
+    c = st["case"]
+    page, G, d = c["page"], c["G"], c["d"]
+    out = torch.zeros(st["q"].shape, dtype=torch.float64, device="cuda")
+    for b in range(c["B"]):
+        L, n = st["host_lens"][b], st["host_counts"][b]
+        pages = st["table"][b, :(L + page - 1) // page].tolist()
+        if not pages:
+            continue
+        for h in range(c["Hkv"]):
+            k, v = (_exact_values(torch.cat([st[s + "_codes"][p, h] for p in pages])[:L],
+                                  torch.cat([st[s + "_scales"][p, h] for p in pages])[:L], c["g"])
+                    for s in "kv")
+            for i in range(n):
+                q = st["q"][b, i, h * G:(h + 1) * G].double()
+                upto = L - n + i + 1
+                out[b, i, h * G:(h + 1) * G] = torch.softmax(q @ k[:upto].T * st["scale"], dim=-1) @ v[:upto]
+    return out
+
+
+def exact(case, seed):
+    global own
+    if case["kind"] not in ("store", "attend"):
+        return None  # whole numbers and bytes only
+    was, own = own, False
+    try:
+        st = prepare(case, seed)
+    finally:
+        own = was
+    return _exact_store(st) if case["kind"] == "store" else _exact_attend(st)
