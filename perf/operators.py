@@ -446,7 +446,7 @@ def run(state):
         if own:
             tq.tq_pages_free(st["pool"], st["leaving"])
             tq.tq_pages_fork(st["pool"], st["arrays"], st["parent_of"], st["status"][0:1], st["ws"])
-            tq.tq_pages_extend(st["pool"], st["need"], st["status"][1:2], st["ws"])
+            tq.tq_pages_extend(st["pool"], st["need"], st["status"][1:2])
         else:
             _plain_free(st, st["leaving"])
             _plain_fork(st, st["parent_of"], st["status"][0])
@@ -454,8 +454,8 @@ def run(state):
     else:  # a wave of requests comes and goes, a later one stays: its pages are packed; then a snapshot
         if own:
             tq.tq_pages_free(st["pool"], st["is_late"])
-            tq.tq_pages_extend(st["pool"], st["need_short"], st["status"][0:1], st["ws"])
-            tq.tq_pages_extend(st["pool"], st["need_late"], st["status"][1:2], st["ws"])
+            tq.tq_pages_extend(st["pool"], st["need_short"], st["status"][0:1])
+            tq.tq_pages_extend(st["pool"], st["need_late"], st["status"][1:2])
             tq.tq_pages_free(st["pool"], st["is_short"])
             tq.tq_pages_compact(st["pool"], st["arrays"], st["live"], st["ws"])
             tq.tq_pages_copy(st["arrays"], st["copy_src"], st["copy_dst"])
