@@ -289,6 +289,134 @@ int tq_decode_attention_paged(const void *q, int dtype, int Hq, const int *T_len
 int tq_prefill_attention(const void *q, int dtype, int Hq, int Lq, int t0, float scale,
                          const tq_cache *cache, float *out, void *stream);
 
+/* ---------------------------------------------------------------- microscaled 4-bit cache
+ *
+ * A paged cache whose keys and values are Blackwell's FP4 numbers with block scales: 16
+ * consecutive elements of a head share one E4M3 scale, a tensor one float scale ("Where This Fits
+ * in the Inference Stack", Blackwell FP4, in the hardware's own microscaled form: no rotation, no
+ * codebook, no per-vector norm). A block x with top = max |x| is stored as
+ *   S    = E4M3(min(top / (6 g), 448))        one byte, to nearest, ties to even
+ *   code = E2M1(x_i / (S g))                  4 bits, to nearest, ties to even, saturating at 6
+ * and stands for E2M1 * S * g. Blocks whose top is below about 2^-10 * 6 g have S = 0 and stand
+ * for zeros; a NaN or infinity in a block makes its S NaN (0x7F), so that it stays visible.
+ *
+ * Per tensor, in pages of page_size positions (a power of two, >= 16):
+ *   codes  [num_pages][Hkv][page_size][d/2]   uint8  element 2j in the low half of byte j
+ *   scales [num_pages][Hkv][page_size][d/16]  uint8  E4M3 bytes
+ *   block_table [B][max_pages] int32: page of each logical page; an entry outside
+ *     0..num_pages-1 (-1, say) is an unmapped page: writes to it are dropped, reads give zeros,
+ *     attention does not see it.
+ * d is 64, 128 or 256; k_scale and v_scale (g) lie in 2^-64..2^64. All lengths and tables are
+ * read on the device when the kernels run, so captured graphs follow them.
+ *
+ * Rows of a batch: the calls below take `rows` rows of every sequence (T new tokens, Lq queries),
+ * left-aligned, and the lengths AFTER them: row t < n_b of sequence b is position
+ * lens[b] - n_b + t, with n_b = clamp(counts[b], 0, rows), or rows where counts is NULL. lens and
+ * counts are DEVICE arrays of B int32 (4-byte aligned). Rows t >= n_b belong to no sequence. */
+typedef struct {
+  int B, Hkv, d, page_size, num_pages, max_pages;
+  float k_scale, v_scale;
+  uint8_t *k_codes, *v_codes;
+  uint8_t *k_scales, *v_scales;
+  const int32_t *block_table;
+} tq_mx_cache;
+
+/* Quantise T rows of keys and values (either NULL to write only the other; device) into their
+ * pages. Element (b, h, t, i) of K is K[b s0 + h s1 + t s2 + i] with k_strides = {s0, s1, s2} (host
+ * array, in elements, each >= 0 and a multiple of 16 bytes; NULL: contiguous [B][Hkv][T][d]), so that slices
+ * of a fused projection need no copy. Rows of no sequence, negative positions and positions past
+ * max_pages * page_size or on unmapped pages are dropped; all other records stay as they were.
+ * Two sequences must not write to one shared page (tq_pages_fork gives each its own).
+ * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (d, dtype), TQ_ERR_CUDA. T = 0 is a no-op. */
+int tq_quantize_kv_mx(const void *K, const void *V, int dtype, int T, const int64_t *k_strides,
+                      const int64_t *v_strides, const int32_t *lens, const int32_t *counts,
+                      const tq_mx_cache *cache, void *stream);
+
+/* The counterpart: write the values of the same rows to K, V (contiguous [B][Hkv][T][d] of `dtype`,
+ * device, either NULL). Rows that tq_quantize_kv_mx would drop read as zeros. With counts = lens
+ * (and T >= every length) this is the whole sequence. */
+int tq_dequantize_mx(const tq_mx_cache *cache, int T, const int32_t *lens, const int32_t *counts, void *K,
+                     void *V, int dtype, void *stream);
+
+/* Attention of Lq queries of every sequence over the cache, their own tokens already written: the
+ * decode step (Lq = 1), drafts being verified, short chunks. q [B][Lq][Hq][d] of `dtype` (TQ_BF16
+ * or TQ_F16), out [B][Lq][Hq][d] of `out_dtype` (any of the three types). Query i of sequence b
+ * stands at position lens[b] - n_b + i and sees the mapped cache positions up to its own;
+ * a query that sees none, and rows of no sequence, give zeros. What a query does not see cannot
+ * reach its output, NaN included. Sums and softmax in fp32; keys, values and queries enter the
+ * tensor cores exactly (fp16 products of 6- and 11-bit significands), softmax weights in fp16.
+ * Lq is 1..16, Hq a multiple of Hkv. The workspace depends on d only (not on the lengths, Hq or
+ * Lq): one serves decode steps and drafts in turn; calls that may overlap on the GPU need one each. Errors: TQ_ERR_INVALID_ARG,
+ * TQ_ERR_UNSUPPORTED, TQ_ERR_WORKSPACE, TQ_ERR_CUDA. */
+size_t tq_decode_mx_workspace_bytes(int Hq, int Lq, const tq_mx_cache *cache);
+int tq_decode_attention_mx(const void *q, int dtype, int Hq, int Lq, const int32_t *lens, const int32_t *counts,
+                           float scale, const tq_mx_cache *cache, void *out, int out_dtype, void *ws,
+                           size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------- pages of paged caches
+ *
+ * Which sequence holds which page, on the device ("Why the KV Cache Exists", PagedAttention and
+ * prefix caching). One pool serves the caches of all layers: they share its block table, and page
+ * p of every layer's arrays belongs together. All arrays are device pointers of the caller:
+ *   refs        [num_pages] int32       sequences (or other holders) of each page; 0 = free
+ *   block_table [B][max_pages] int32    pages of each sequence, -1 behind its last
+ *   lens        [B] int32               positions of each sequence
+ * A fresh pool has refs 0, block_table -1, lens 0. A caller may hold pages itself by raising refs.
+ * page_size is a power of two >= 16, max_pages * page_size <= 2^30, B <= 4096.
+ *
+ * The calls are functions of the pool's state when they run; they are ordered by the stream and
+ * must not overlap with each other or with users of the same pool. `status` (device int32, 4-byte
+ * aligned) gets 0, or why nothing was changed: 1 = not enough free pages, 2 = a sequence would
+ * pass max_pages. The workspace (tq_pages_workspace_bytes) is scratch between calls. */
+typedef struct {
+  int B, max_pages, num_pages, page_size;
+  int32_t *refs, *block_table, *lens;
+} tq_page_pool;
+
+/* One array of a cache: page p is bytes [p page_bytes, (p + 1) page_bytes) from base (both
+ * multiples of 16; page_bytes < 2^31). At most 1024 of them (all layers') in a call. */
+typedef struct {
+  void *base;
+  size_t page_bytes;
+} tq_page_array;
+
+/* The page arrays of a cache: writes up to 8 of them (host memory) and returns how many (0 on
+ * invalid arguments). Concatenate the layers' for the calls below. */
+int tq_paged_cache_arrays(const tq_paged_cache *cache, tq_page_array *out);
+int tq_mx_cache_arrays(const tq_mx_cache *cache, tq_page_array *out);
+
+size_t tq_pages_workspace_bytes(const tq_page_pool *pool);
+
+/* Add max(need[b], 0) positions to every sequence (need: device int32 [B]): lens[b] grows by it and
+ * the pages it takes are the lowest-numbered free ones, in the order of (b, logical page). */
+int tq_pages_extend(const tq_page_pool *pool, const int32_t *need, int32_t *status, void *stream);
+
+/* Sequence b becomes a copy of sequence parent_of[b] (device int32 [B]; values outside 0..B-1, and
+ * b itself: b stays as it is). All parents are read as they were, so rows may swap. The child's
+ * old pages are given back; it shares the parent's full pages (refs + 1) and gets its own copy of
+ * a partly filled last page, the lowest-numbered pages free at entry in the order of b, copied in
+ * all arrays. n_arrays may be 0 (bookkeeping only). */
+int tq_pages_fork(const tq_page_pool *pool, const tq_page_array *arrays, int n_arrays,
+                  const int32_t *parent_of, int32_t *status, void *ws, size_t ws_bytes, void *stream);
+
+/* Sequences with leaving[b] != 0 (device int32 [B]) give their pages back: refs - 1 for each, rows
+ * -1, lens 0. */
+int tq_pages_free(const tq_page_pool *pool, const int32_t *leaving, void *stream);
+
+/* Pack the live pages (refs != 0) into the first *live (device int32, 4-byte aligned) pages of the
+ * pool: the k-th highest live page at or above *live moves to the k-th lowest free page below it,
+ * in all arrays, with its refs; the block table follows. Pages that a caller holds by number move
+ * too. */
+int tq_pages_compact(const tq_page_pool *pool, const tq_page_array *arrays, int n_arrays, int32_t *live,
+                     void *ws, size_t ws_bytes, void *stream);
+
+/* Copy pages src[i] to dst[i], i < n (HOST arrays, read during the call), in all arrays of caches of
+ * num_pages pages. Every index must lie in 0..num_pages-1, the dst be distinct, and none of them
+ * a src (TQ_ERR_INVALID_ARG otherwise, nothing launched): the pages of the copies do not depend
+ * on their order. */
+int tq_pages_copy(const tq_page_array *arrays, int n_arrays, int num_pages, const int *src, const int *dst,
+                  int n, void *stream);
+
 /* Device-side faults recorded since the last call, as bits: bit 0 = a tensor-core kernel
  * (tcgen05 write path of TurboQuant_prod records) gave up waiting for its MMAs after about a
  * second, recorded a fault, freed its tensor memory and returned without writing the rest of

@@ -14,11 +14,11 @@
 #include <string>
 
 namespace {
-
 thread_local std::string g_err;
+}
 
-int fail(int code, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
-int fail(int code, const char *fmt, ...) {
+// Records the message of tq_last_error and returns `code` (shared with host_mx.cpp).
+int tq::fail(int code, const char *fmt, ...) {
   char buf[512];
   va_list ap;
   va_start(ap, fmt);
@@ -27,6 +27,10 @@ int fail(int code, const char *fmt, ...) {
   g_err = buf;
   return code;
 }
+
+namespace {
+
+using tq::fail;
 
 // ---------------------------------------------------------------- SplitMix64
 // Steele, Lea & Flood, "Fast splittable pseudorandom number generators" (OOPSLA 2014):

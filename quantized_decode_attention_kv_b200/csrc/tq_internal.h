@@ -6,6 +6,8 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "../../include/tq.h"
+
 namespace tq {
 
 constexpr int kMaxM = 256;       // longest QJL sketch supported
@@ -177,5 +179,62 @@ cudaError_t launch_prod_decode(const DecodeArgs &a, cudaStream_t s);
 bool bf16_decode_supported(int d, int G);
 void plan_bf16_mma(int B, int Hq, int Hkv, int T_len, int sm_count, DecodePlan *p);
 cudaError_t launch_bf16_mma(const DecodeBf16Args &a, cudaStream_t s);
+
+// Error text of the calling thread (host.cpp): records the message, returns `code`.
+int fail(int code, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
+
+// ---------------------------------------------------------------- microscaled 4-bit paged cache
+// Row t < count(b) of a batch sits at position lens[b] - count(b) + t of sequence b, where
+// count(b) = clamp(counts[b], 0, rows) (rows when counts is NULL).
+struct MxCacheArgs {
+  int B, Hkv, d, pshift, maxp, num_pages;
+  float g[2];                    // tensor scales of keys and values
+  uint8_t *codes[2], *scales[2]; // keys, values
+  const int *bt;
+};
+
+struct MxRowsArgs { // write (x -> pages) or read (pages -> x) of up to T rows of each sequence
+  MxCacheArgs c;
+  void *x[2];          // keys, values (NULL: skipped)
+  long long st[2][3];  // strides of x in elements: sequence, head, row
+  int dtype, T;
+  const int *lens, *counts;
+};
+cudaError_t launch_mx_write(const MxRowsArgs &a, cudaStream_t s);
+cudaError_t launch_mx_read(const MxRowsArgs &a, cudaStream_t s);
+
+struct MxPlan {
+  int nt;         // tiles of 8 query rows (query, head of the group) that a CTA holds
+  int row_blocks; // blocks of 8 nt rows per (sequence, KV head)
+  int ctas;
+  size_t ws_bytes;
+};
+struct MxDecodeArgs {
+  MxCacheArgs c;
+  const void *q;
+  int dtype, Hq, Lq, out_dtype;
+  const int *lens, *counts;
+  float scale;
+  void *out;
+  void *ws;
+  MxPlan plan;
+};
+MxPlan plan_mx_decode(int Hkv, int d, int Hq, int Lq, int sm_count);
+cudaError_t launch_mx_decode(const MxDecodeArgs &a, cudaStream_t s);
+
+// ---------------------------------------------------------------- pages of paged caches
+constexpr int kMaxPoolB = 4096;       // sequences of a page pool
+constexpr int kMaxPageArrays = 1024;  // arrays (over all layers) that one call moves pages of
+constexpr int kPageCopyBatch = 512;   // (source, destination) pairs in one launch's parameters
+
+cudaError_t launch_pages_extend(const tq_page_pool &p, const int *need, int *status, cudaStream_t s);
+cudaError_t launch_pages_fork(const tq_page_pool &p, const tq_page_array *arrays, int n_arrays,
+                              const int *parent_of, int *status, void *ws, int sm_count, cudaStream_t s);
+cudaError_t launch_pages_free(const tq_page_pool &p, const int *leaving, cudaStream_t s);
+cudaError_t launch_pages_compact(const tq_page_pool &p, const tq_page_array *arrays, int n_arrays, int *live,
+                                 void *ws, int sm_count, cudaStream_t s);
+cudaError_t launch_pages_copy(const tq_page_array *arrays, int n_arrays, const int *src, const int *dst, int n,
+                              int sm_count, cudaStream_t s);
+size_t pages_workspace_bytes(const tq_page_pool &p);
 
 } // namespace tq

@@ -59,6 +59,28 @@ class tq_paged_cache(ctypes.Structure):
     ]
 
 
+class tq_mx_cache(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int), ("page_size", ctypes.c_int),
+        ("num_pages", ctypes.c_int), ("max_pages", ctypes.c_int),
+        ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
+        ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p),
+    ]
+
+
+class tq_page_pool(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int), ("max_pages", ctypes.c_int), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+        ("refs", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+    ]
+
+
+class tq_page_array(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_size_t)]
+
+
 EXPORTS = {
     # name: (restype, argtypes)
     "tq_last_error": (ctypes.c_char_p, []),
@@ -107,6 +129,30 @@ EXPORTS = {
                                                 ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                                 ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p,
                                                 ctypes.c_size_t, ctypes.c_void_p]),
+    "tq_quantize_kv_mx": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_int,
+                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                         ctypes.POINTER(tq_mx_cache), ctypes.c_void_p]),
+    "tq_dequantize_mx": (ctypes.c_int, [ctypes.POINTER(tq_mx_cache), ctypes.c_int, ctypes.c_void_p,
+                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                        ctypes.c_void_p]),
+    "tq_decode_mx_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int, ctypes.c_int, ctypes.POINTER(tq_mx_cache)]),
+    "tq_decode_attention_mx": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                              ctypes.c_void_p, ctypes.c_void_p, ctypes.c_float,
+                                              ctypes.POINTER(tq_mx_cache), ctypes.c_void_p, ctypes.c_int,
+                                              ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "tq_paged_cache_arrays": (ctypes.c_int, [ctypes.POINTER(tq_paged_cache), ctypes.POINTER(tq_page_array)]),
+    "tq_mx_cache_arrays": (ctypes.c_int, [ctypes.POINTER(tq_mx_cache), ctypes.POINTER(tq_page_array)]),
+    "tq_pages_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(tq_page_pool)]),
+    "tq_pages_extend": (ctypes.c_int, [ctypes.POINTER(tq_page_pool), ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_void_p]),
+    "tq_pages_fork": (ctypes.c_int, [ctypes.POINTER(tq_page_pool), ctypes.POINTER(tq_page_array), ctypes.c_int,
+                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                     ctypes.c_void_p]),
+    "tq_pages_free": (ctypes.c_int, [ctypes.POINTER(tq_page_pool), ctypes.c_void_p, ctypes.c_void_p]),
+    "tq_pages_compact": (ctypes.c_int, [ctypes.POINTER(tq_page_pool), ctypes.POINTER(tq_page_array), ctypes.c_int,
+                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "tq_pages_copy": (ctypes.c_int, [ctypes.POINTER(tq_page_array), ctypes.c_int, ctypes.c_int, ctypes.c_void_p,
+                                     ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p]),
 }
 
 
@@ -440,6 +486,241 @@ def tq_decode_attention_bf16(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, 
     _check(lib.tq_decode_attention_bf16(_dev(q, "q"), q.shape[1], _dev(K, "K"), _dev(V, "V"), B, Hkv, T_cap,
                                         T_len, d, scale, _dev(out, "out"), _dev(ws, "ws"),
                                         ws.numel() * ws.element_size(), _stream(stream)))
+
+
+# ------------------------------------------------------------------ microscaled 4-bit paged cache
+class TQMXCache:
+    """One layer's microscaled 4-bit paged cache (E2M1 elements, an E4M3 scale for each 16, one float
+    scale per tensor): torch owns the page pools; ``block_table`` is an int32 [B][max_pages] device
+    tensor (a page pool's, or the caller's own), read when the kernels run. Shapes follow
+    include/tq.h."""
+
+    def __init__(self, B: int, Hkv: int, d: int, page_size: int, num_pages: int, max_pages: int,
+                 block_table: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0):
+        if (not isinstance(block_table, torch.Tensor) or block_table.dtype != torch.int32 or not block_table.is_cuda
+                or tuple(block_table.shape) != (B, max_pages) or not block_table.is_contiguous()):
+            raise TQError(TQ_ERR_INVALID_ARG, "block_table must be a contiguous int32 CUDA tensor [B][max_pages]")
+        self.B, self.Hkv, self.d, self.page_size = B, Hkv, d, page_size
+        self.num_pages, self.max_pages, self.k_scale, self.v_scale = num_pages, max_pages, k_scale, v_scale
+        self.block_table, self.device = block_table, block_table.device
+        shape = (num_pages, Hkv, page_size)
+        self.tensors = {}
+        for side in "kv":
+            self.tensors[f"{side}_codes"] = torch.zeros(shape + (d // 2,), dtype=torch.uint8, device=self.device)
+            self.tensors[f"{side}_scales"] = torch.zeros(shape + (d // 16,), dtype=torch.uint8, device=self.device)
+        t = self.tensors
+        self.struct = tq_mx_cache(B, Hkv, d, page_size, num_pages, max_pages, k_scale, v_scale,
+                                  t["k_codes"].data_ptr(), t["v_codes"].data_ptr(), t["k_scales"].data_ptr(),
+                                  t["v_scales"].data_ptr(), block_table.data_ptr())
+        if int(lib.tq_mx_cache_arrays(ctypes.byref(self.struct), (tq_page_array * 8)())) == 0:
+            raise TQError(TQ_ERR_INVALID_ARG, last_error())
+
+    def __getitem__(self, key):
+        return self.tensors[key]
+
+
+def _run(fn, device: torch.device, stream, *args) -> None:
+    """Call a libtq entry point with ``device`` current, on ``stream`` (default: the device's
+    current stream)."""
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(stream)))
+
+
+def _i32(t, n: int, name: str, device: torch.device) -> int:
+    """Pointer of a contiguous int32 tensor of n elements on the device (n < 0: at least one)."""
+    if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device or not t.is_contiguous()
+            or (t.dim() != 1 or t.shape[0] != n if n >= 0 else t.numel() < 1)):
+        raise TQError(TQ_ERR_INVALID_ARG, f"{name} must be a contiguous int32 tensor"
+                      f"{f' [{n}]' if n >= 0 else ''} on {device}")
+    return t.data_ptr()
+
+
+def _mx_rows(x, cache: TQMXCache, name: str, contiguous: bool):
+    """Checks one [B, Hkv, T, d] tensor; its (pointer, strides in elements)."""
+    if x is None:
+        return None, None
+    if (not isinstance(x, torch.Tensor) or x.device != cache.device or x.dim() != 4 or x.shape[0] != cache.B
+            or x.shape[1] != cache.Hkv or x.shape[3] != cache.d):
+        raise TQError(TQ_ERR_INVALID_ARG, f"{name} must be a tensor [B={cache.B}][Hkv={cache.Hkv}][T][d={cache.d}] "
+                      f"on {cache.device}")
+    if contiguous:
+        if not x.is_contiguous():
+            raise TQError(TQ_ERR_INVALID_ARG, f"{name} must be contiguous")
+        return x.data_ptr(), None
+    s = x.stride()
+    if s[3] != 1:
+        raise TQError(TQ_ERR_INVALID_ARG, f"{name}: the elements of a row must be adjacent")
+    return x.data_ptr(), (ctypes.c_int64 * 3)(s[0], s[1], s[2])
+
+
+def _mx_pair(K, V, cache: TQMXCache, contiguous: bool):
+    ref = K if K is not None else V
+    if ref is None:
+        raise TQError(TQ_ERR_INVALID_ARG, "K and V are both None")
+    kp, ks = _mx_rows(K, cache, "K", contiguous)
+    vp, vs = _mx_rows(V, cache, "V", contiguous)
+    if K is not None and V is not None and (K.dtype != V.dtype or K.shape[2] != V.shape[2]):
+        raise TQError(TQ_ERR_INVALID_ARG, "K and V must share their dtype and T")
+    dt = _DTYPES.get(ref.dtype)
+    if dt is None:
+        raise TQError(TQ_ERR_INVALID_ARG, f"unsupported dtype {ref.dtype}")
+    return kp, ks, vp, vs, dt, ref.shape[2]
+
+
+def tq_quantize_kv_mx(K: torch.Tensor | None, V: torch.Tensor | None, cache: TQMXCache, lens: torch.Tensor,
+                      counts: torch.Tensor | None = None, stream=None) -> None:
+    """Write rows of K, V [B, Hkv, T, d] (any strides whose rows are adjacent and 16-byte aligned): row
+    t < counts[b] (default: T) is position lens[b] - counts[b] + t of sequence b; lens holds the
+    lengths after the write. lens, counts: int32 [B] on the device."""
+    kp, ks, vp, vs, dt, T = _mx_pair(K, V, cache, False)
+    dev = cache.device
+    _run(lib.tq_quantize_kv_mx, dev, stream, kp, vp, dt, T, ks, vs, _i32(lens, cache.B, "lens", dev),
+         None if counts is None else _i32(counts, cache.B, "counts", dev), ctypes.byref(cache.struct))
+
+
+def tq_dequantize_mx(cache: TQMXCache, lens: torch.Tensor, K: torch.Tensor | None, V: torch.Tensor | None,
+                     counts: torch.Tensor | None = None, stream=None) -> None:
+    """Read the same rows back into K, V (contiguous [B, Hkv, T, d]); rows that hold none are zeros."""
+    kp, _, vp, _, dt, T = _mx_pair(K, V, cache, True)
+    dev = cache.device
+    _run(lib.tq_dequantize_mx, dev, stream, ctypes.byref(cache.struct), T, _i32(lens, cache.B, "lens", dev),
+         None if counts is None else _i32(counts, cache.B, "counts", dev), kp, vp, dt)
+
+
+def tq_decode_mx_workspace_bytes(cache: TQMXCache, Hq: int, Lq: int = 1) -> int:
+    if cache.device.index == torch.cuda.current_device():
+        n = int(lib.tq_decode_mx_workspace_bytes(Hq, Lq, ctypes.byref(cache.struct)))
+    else:
+        with torch.cuda.device(cache.device):
+            n = int(lib.tq_decode_mx_workspace_bytes(Hq, Lq, ctypes.byref(cache.struct)))
+    if n == 0:
+        raise TQError(TQ_ERR_INVALID_ARG, last_error())
+    return n
+
+
+def tq_decode_attention_mx(q: torch.Tensor, cache: TQMXCache, lens: torch.Tensor, scale: float, out: torch.Tensor,
+                           ws: torch.Tensor, counts: torch.Tensor | None = None, stream=None) -> None:
+    """Attention of q [B, Lq, Hq, d] (bf16 or fp16, Lq <= 16) over the cache: query i < counts[b]
+    (default: Lq) stands at position lens[b] - counts[b] + i and sees the positions up to its own;
+    out [B, Lq, Hq, d] (any dtype). Queries that see nothing give zeros."""
+    dev = cache.device
+    if (not isinstance(q, torch.Tensor) or q.dim() != 4 or q.shape[0] != cache.B or q.shape[3] != cache.d
+            or q.device != dev or not q.is_contiguous()):
+        raise TQError(TQ_ERR_INVALID_ARG, f"q must be a contiguous tensor [B={cache.B}][Lq][Hq][d={cache.d}] on {dev}")
+    if not isinstance(out, torch.Tensor) or out.shape != q.shape or out.device != dev or not out.is_contiguous():
+        raise TQError(TQ_ERR_INVALID_ARG, f"out must be a contiguous tensor of q's shape on {dev}")
+    dt, odt = _DTYPES.get(q.dtype), _DTYPES.get(out.dtype)
+    if dt is None or odt is None:
+        raise TQError(TQ_ERR_INVALID_ARG, f"unsupported dtypes {q.dtype}, {out.dtype}")
+    if ws.device != dev:
+        raise TQError(TQ_ERR_INVALID_ARG, f"ws must be on {dev}")
+    _run(lib.tq_decode_attention_mx, dev, stream, q.data_ptr(), dt, q.shape[2], q.shape[1],
+         _i32(lens, cache.B, "lens", dev), None if counts is None else _i32(counts, cache.B, "counts", dev), scale,
+         ctypes.byref(cache.struct), out.data_ptr(), odt, _dev(ws, "ws"), ws.numel() * ws.element_size())
+
+
+# ------------------------------------------------------------------ pages of paged caches
+class TQPagePool:
+    """Reference counts, block table and lengths of the sequences of paged caches, on the device (a
+    fresh pool: every page free, every sequence empty). Give ``block_table`` to the caches of all
+    layers (TQPagedCache or TQMXCache)."""
+
+    def __init__(self, B: int, max_pages: int, num_pages: int, page_size: int, device: str = "cuda"):
+        dev = torch.device(device)
+        self.B, self.max_pages, self.num_pages, self.page_size = B, max_pages, num_pages, page_size
+        self.refs = torch.zeros(num_pages, dtype=torch.int32, device=dev)
+        self.block_table = torch.full((B, max_pages), -1, dtype=torch.int32, device=dev)
+        self.lens = torch.zeros(B, dtype=torch.int32, device=dev)
+        self.device = self.refs.device
+        self.struct = tq_page_pool(B, max_pages, num_pages, page_size, self.refs.data_ptr(),
+                                   self.block_table.data_ptr(), self.lens.data_ptr())
+        tq_pages_workspace_bytes(self)  # checks the shape
+
+
+class TQPageArrays:
+    """The page arrays of one or more caches (all layers'), as the page moves take them; build once."""
+
+    def __init__(self, caches):
+        self.caches = list(caches)  # keeps the memory alive
+        found = []
+        for c in self.caches:
+            part = (tq_page_array * 8)()
+            fn = lib.tq_mx_cache_arrays if isinstance(c, TQMXCache) else lib.tq_paged_cache_arrays
+            n = int(fn(ctypes.byref(c.struct), part))
+            if n == 0:
+                raise TQError(TQ_ERR_INVALID_ARG, last_error())
+            found.extend(part[:n])
+        shapes = {(c.num_pages, c.page_size) for c in self.caches}
+        if len(shapes) != 1:
+            raise TQError(TQ_ERR_INVALID_ARG, f"caches must share num_pages and page_size, got {sorted(shapes)}")
+        (self.num_pages, self.page_size), = shapes
+        self.n = len(found)
+        self.arrays = (tq_page_array * self.n)(*found)
+        self.device = self.caches[0].block_table.device
+        if any(c.block_table.device != self.device for c in self.caches):
+            raise TQError(TQ_ERR_INVALID_ARG, "caches must be on one device")
+
+
+def tq_page_arrays(caches) -> TQPageArrays:
+    return TQPageArrays([caches] if isinstance(caches, (TQMXCache, TQPagedCache)) else caches)
+
+
+def tq_pages_workspace_bytes(pool: TQPagePool) -> int:
+    n = int(lib.tq_pages_workspace_bytes(ctypes.byref(pool.struct)))
+    if n == 0:
+        raise TQError(TQ_ERR_INVALID_ARG, last_error())
+    return n
+
+
+def _pool_arrays(pool: TQPagePool, arrays: TQPageArrays | None):
+    if arrays is None:
+        return None, 0
+    if (arrays.num_pages, arrays.page_size, arrays.device) != (pool.num_pages, pool.page_size, pool.device):
+        raise TQError(TQ_ERR_INVALID_ARG, "arrays must have the pool's num_pages, page_size and device")
+    return arrays.arrays, arrays.n
+
+
+def tq_pages_extend(pool: TQPagePool, need: torch.Tensor, status: torch.Tensor, stream=None) -> None:
+    """lens[b] += need[b] (int32 [B]), with the lowest free pages. status (int32, one element): 0, or
+    1 (not enough free pages) or 2 (a sequence would pass max_pages) and nothing changed."""
+    _run(lib.tq_pages_extend, pool.device, stream, ctypes.byref(pool.struct), _i32(need, pool.B, "need", pool.device),
+         _i32(status, -1, "status", pool.device))
+
+
+def tq_pages_fork(pool: TQPagePool, arrays: TQPageArrays | None, parent_of: torch.Tensor, status: torch.Tensor,
+                  ws: torch.Tensor, stream=None) -> None:
+    """Sequence b becomes a copy of sequence parent_of[b] (int32 [B]; -1: stays): full pages shared, a
+    partly filled last page copied in all arrays."""
+    ap, n = _pool_arrays(pool, arrays)
+    _run(lib.tq_pages_fork, pool.device, stream, ctypes.byref(pool.struct), ap, n,
+         _i32(parent_of, pool.B, "parent_of", pool.device), _i32(status, -1, "status", pool.device), _dev(ws, "ws"),
+         ws.numel() * ws.element_size())
+
+
+def tq_pages_free(pool: TQPagePool, leaving: torch.Tensor, stream=None) -> None:
+    """Sequences with leaving[b] != 0 (int32 [B]) give their pages back."""
+    _run(lib.tq_pages_free, pool.device, stream, ctypes.byref(pool.struct),
+         _i32(leaving, pool.B, "leaving", pool.device))
+
+
+def tq_pages_compact(pool: TQPagePool, arrays: TQPageArrays | None, live: torch.Tensor, ws: torch.Tensor,
+                     stream=None) -> None:
+    """Pack the live pages into the first ``live`` (int32, one element, written) pages of the pool."""
+    ap, n = _pool_arrays(pool, arrays)
+    _run(lib.tq_pages_compact, pool.device, stream, ctypes.byref(pool.struct), ap, n,
+         _i32(live, -1, "live", pool.device), _dev(ws, "ws"), ws.numel() * ws.element_size())
+
+
+def tq_pages_copy(arrays: TQPageArrays, src, dst, stream=None) -> None:
+    """Copy pages src[i] to dst[i] (host integers) in all arrays; dst distinct and none of them a src."""
+    s, t = (np.ascontiguousarray(x, dtype=np.int32) for x in (src, dst))
+    if s.ndim != 1 or s.shape != t.shape:
+        raise TQError(TQ_ERR_INVALID_ARG, "src and dst must be equally long lists of page numbers")
+    _run(lib.tq_pages_copy, arrays.device, stream, arrays.arrays, arrays.n, arrays.num_pages, s.ctypes.data,
+         t.ctypes.data, s.shape[0])
 
 
 def workspace(nbytes: int, device="cuda") -> torch.Tensor:
