@@ -50,10 +50,10 @@ int check_mx(const tq_mx_cache *c, tq::MxCacheArgs *a) {
   if (shift < 0) return fail(TQ_ERR_INVALID_ARG, "page_size=%d must be a power of two >= 16", c->page_size);
   if (static_cast<long long>(c->max_pages) * c->page_size > (1ll << 30))
     return fail(TQ_ERR_INVALID_ARG, "max_pages=%d pages of %d positions pass 2^30", c->max_pages, c->page_size);
-  // the attention kernel numbers records in 32 bits; a pool of 2^32 records does not fit on a GPU
-  if (static_cast<double>(c->num_pages) * c->Hkv * c->page_size >= 4294967296.0)
-    return fail(TQ_ERR_INVALID_ARG, "pool of %d pages x %d heads x %d positions: must be below 2^32 records",
-                c->num_pages, c->Hkv, c->page_size);
+  // the attention kernel numbers 16-byte chunks of codes in 32 bits: 64 GiB an array
+  if (static_cast<double>(c->num_pages) * c->Hkv * c->page_size * (c->d / 2) > 0x1p36)
+    return fail(TQ_ERR_INVALID_ARG, "pool of %d pages x %d heads x %d positions of d=%d: codes pass 64 GiB",
+                c->num_pages, c->Hkv, c->page_size, c->d);
   const float lo = 0x1p-64f, hi = 0x1p64f;
   if (!(c->k_scale >= lo && c->k_scale <= hi) || !(c->v_scale >= lo && c->v_scale <= hi))
     return fail(TQ_ERR_INVALID_ARG, "k_scale=%g and v_scale=%g must lie in 2^-64..2^64", c->k_scale, c->v_scale);
@@ -108,9 +108,10 @@ int check_decode_shape(int Hq, int Lq, const tq_mx_cache *cache, tq::MxDecodeArg
   if (Hq < 1 || Hq % cache->Hkv || Hq > 65535)
     return fail(TQ_ERR_INVALID_ARG, "Hq=%d must be a positive multiple of Hkv=%d (<= 65535)", Hq, cache->Hkv);
   if (Lq < 1 || Lq > 16) return fail(TQ_ERR_INVALID_ARG, "Lq=%d: must be 1..16 queries a sequence", Lq);
-  // the kernel numbers 16-position tiles over all sequences and blocks of 8 rows in 64 bits
-  const double rows = static_cast<double>(Lq) * (Hq / cache->Hkv);
-  if (static_cast<double>(cache->B) * cache->Hkv * (rows / 8 + 1) * cache->max_pages * cache->page_size >= 0x1p56)
+  // the kernel numbers 16-position tiles over all sequences and row blocks (of 8 rows at least) in 32 bits
+  const double blocks = std::ceil(static_cast<double>(Lq) * (Hq / cache->Hkv) / 8);
+  const double tiles = static_cast<double>(cache->max_pages) * (cache->page_size / 16) + 4;
+  if (cache->B * blocks * cache->Hkv * tiles >= 4294967296.0)
     return fail(TQ_ERR_INVALID_ARG, "B=%d x Hkv=%d x %d positions are too many for one call", cache->B, cache->Hkv,
                 cache->max_pages * cache->page_size);
   int sms = 0;
@@ -160,7 +161,7 @@ extern "C" {
 int tq_quantize_kv_mx(const void *K, const void *V, int dtype, int T, const int64_t *k_strides,
                       const int64_t *v_strides, const int32_t *lens, const int32_t *counts,
                       const tq_mx_cache *cache, void *stream) {
-  tq::MxRowsArgs a;
+  tq::MxRowsArgs a{};
   int st = check_rows(K, V, dtype, T, lens, counts, cache, &a);
   if (st) return st;
   st = take_strides(k_strides, *cache, T, dtype, "K", a.st[0]);
@@ -173,7 +174,7 @@ int tq_quantize_kv_mx(const void *K, const void *V, int dtype, int T, const int6
 
 int tq_dequantize_mx(const tq_mx_cache *cache, int T, const int32_t *lens, const int32_t *counts, void *K,
                      void *V, int dtype, void *stream) {
-  tq::MxRowsArgs a;
+  tq::MxRowsArgs a{};
   int st = check_rows(K, V, dtype, T, lens, counts, cache, &a);
   if (st) return st;
   for (int i = 0; i < 2; ++i) take_strides(nullptr, *cache, T, dtype, "", a.st[i]);
@@ -182,7 +183,7 @@ int tq_dequantize_mx(const tq_mx_cache *cache, int T, const int32_t *lens, const
 }
 
 size_t tq_decode_mx_workspace_bytes(int Hq, int Lq, const tq_mx_cache *cache) {
-  tq::MxDecodeArgs a;
+  tq::MxDecodeArgs a{};
   return check_decode_shape(Hq, Lq, cache, &a) ? 0 : a.plan.ws_bytes;
 }
 
@@ -198,7 +199,7 @@ int tq_decode_attention_mx(const void *q, int dtype, int Hq, int Lq, const int32
   if (!aligned(lens, 4) || (counts && !aligned(counts, 4)))
     return fail(TQ_ERR_INVALID_ARG, "lens must be non-NULL, lens and counts 4-byte aligned");
   if (!std::isfinite(scale)) return fail(TQ_ERR_INVALID_ARG, "scale is not finite");
-  tq::MxDecodeArgs a;
+  tq::MxDecodeArgs a{};
   int st = check_decode_shape(Hq, Lq, cache, &a);
   if (st) return st;
   st = check_workspace(ws, ws_bytes, a.plan.ws_bytes);
@@ -238,7 +239,7 @@ int tq_paged_cache_arrays(const tq_paged_cache *c, tq_page_array *out) {
 }
 
 int tq_mx_cache_arrays(const tq_mx_cache *c, tq_page_array *out) {
-  tq::MxCacheArgs a;
+  tq::MxCacheArgs a{};
   if (!out) {
     fail(TQ_ERR_INVALID_ARG, "out is NULL");
     return 0;

@@ -27,7 +27,7 @@ __device__ __forceinline__ void e2m1_to_h2(uint32_t w, uint32_t (&r)[4]) {
 // Two E4M3 bytes (low 16 bits of w) as an fp16 pair (exact; 0x7F and 0xFF are NaN).
 __device__ __forceinline__ uint32_t e4m3_to_h2(uint32_t w) {
   uint32_t r;
-  asm("{\n.reg .b16 t;\ncvt.u16.u32 t, %1;\ncvt.rn.f16x2.e4m3x2 %0, t;\n}" : "=r"(r) : "r"(w));
+  asm("{\n.reg .b16 lo, hi;\nmov.b32 {lo, hi}, %1;\ncvt.rn.f16x2.e4m3x2 %0, lo;\n}" : "=r"(r) : "r"(w));
   return r;
 }
 

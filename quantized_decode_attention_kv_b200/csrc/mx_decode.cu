@@ -16,11 +16,15 @@
 // The softmax reference of a row moves only when a score passes it by 2^15 (a vote in the warp);
 // the frequent path has no cross-lane reduction.
 //
-// Work: the (sequence, KV head, row block, 16-token tile) space is flattened and divided evenly
-// over the CTAs on the device, from the lengths in device memory, so a captured graph follows
-// lengths that change and a ragged batch stays balanced. A CTA's warps share each stretch and
-// merge in shared memory; a unit cut by a CTA boundary leaves partials in the workspace for the
+// Work: the space of 16-token tiles of all (sequence, KV head, row block) units is flattened and
+// divided evenly over all warps of the grid on the device, from the lengths in device memory, so a
+// captured graph follows lengths that change and a ragged batch stays balanced. A unit counts
+// kUnitCost tiles more than it has (queries, page table, output). Each warp copies its own tiles
+// with cp.async into a ring of its own, ahead across units, and waits for no other warp until its
+// stretch is done. Units within a stretch are finished by their warp; the others leave partials in
+// shared memory, joined by the CTA, and those cut by a CTA boundary in the workspace, joined by the
 // combine kernel.
+#include <algorithm>
 #include <cfloat>
 
 #include "mma_ops.cuh"
@@ -32,20 +36,33 @@ namespace {
 using namespace mx;
 using namespace mma_ops;
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr float kRefDrop = 11.0f;  // the reference sits 2^11 below the largest score seen ...
 constexpr float kRefSlack = 15.0f; // ... and follows when a weight would pass 2^15 (fp16 ends at 2^16)
 constexpr float kRefEmpty = -FLT_MAX;
-constexpr int kMinTiles = 8; // tiles a CTA gets at least: one for each warp
+constexpr int kUnitCost = 2; // what a unit costs besides its tiles, in tiles
+constexpr int kMinTiles = 3; // tiles a warp gets at least (unit costs included)
+
+// Shapes of the grid: CTAs of an SM, tiles in a warp's ring.
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+template <int D, int NT>
+struct Cfg {
+  static constexpr int kCtas = D == 64 && NT == 1 ? 4 : D == 256 || (D == 128 && NT == 3) ? 2 : 3;
+  static constexpr int kStages = D == 64 || (D == 128 && NT == 3) ? 6 : 4;
+  static constexpr int kTile = 18 * D;                 // bytes: 16 x (D/2 + D/16) of keys and of values
+  static constexpr int kSlot = 8 * NT * (D + 2) * 4;   // bytes of a partial: sums, then (reference, weight sum)
+  static constexpr int kWarpBytes = kStages * kTile + kSlot;
+  static constexpr int kSmem = kWarps * kWarpBytes;
+  static_assert(kSlot <= kStages * kTile && kTile % 16 == 0 && kSlot % 16 == 0, "the tail's partial reuses the ring");
+};
 
 struct Kernel {
   MxCacheArgs c;
   const uint16_t *q;
   const int *lens, *counts;
   void *out;
-  float *part;   // [2 * ctas][8 NT][D + 2]: output sums, then reference and weight sum
-  int4 *desc;    // [ctas]: {sequence, head, row block, number of CTAs} of the unit cut at its end
+  float *part;   // [2 * ctas] partials (Cfg::kSlot)
+  int4 *desc;    // [ctas]: {sequence, head, first row, number of CTAs} of the unit cut at its end
   int Hq, G, Lq, row_blocks, bf16, out_dtype;
   float scale, klog; // softmax scale; log2(e) * key scale (apart: their product may not fit where a row's does)
 };
@@ -53,6 +70,12 @@ struct Kernel {
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   __half2 r = __hmul2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
   return *reinterpret_cast<uint32_t *>(&r);
+}
+// The low halves of a's bytes and the high halves of b's.
+__device__ __forceinline__ uint32_t select_bits(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, 0x0F0F0F0F, 0xE4;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
@@ -99,75 +122,112 @@ template <int D>
 struct Tile {
   uint32_t k[2][D / 32], v[4][D / 64];
   uint32_t ks[2], vs[4];
-  bool mapped;
 };
 
-template <int N>
-__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N]) {
+// A tile in a ring: key codes [16][D/2], value codes [16][D/2], key scales [16][D/16], value scales
+// [16][D/16]. The eight 16-byte chunks of a 128-byte line of codes are permuted by the line (XOR), so
+// that the lanes' reads (rows g by tig for keys, tokens 2 tig + i by g for values) meet no bank twice.
+template <int D>
+__device__ __forceinline__ int chunk_swizzle(int line) {
+  return D == 64 ? 2 * (line & 1) : D == 128 ? 2 * (line & 3) : line & 7;
+}
+template <int D>
+__device__ __forceinline__ int code_offset(int token, int byte) { // byte: of the token's record, < D/2
+  const int at = token * (D / 2) + byte, line = at >> 7;
+  return line * 128 + ((((at >> 4) & 7) ^ chunk_swizzle<D>(line)) << 4) + (at & 15);
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+template <int N> // 4-byte words
+__device__ __forceinline__ void lds(uint32_t a, uint32_t (&w)[N]) {
   if constexpr (N % 4 == 0) {
 #pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i / 4);
-      w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
-    }
+    for (int i = 0; i < N; i += 4)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]) : "r"(a ^ (4 * i)));
   } else if constexpr (N == 2) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
-    w[0] = v.x, w[1] = v.y;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a));
   } else {
-    w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(a));
   }
 }
-
-template <int N> // N scale bytes (1, 2 or 4)
-__device__ __forceinline__ uint32_t load_scales(const uint8_t *p) {
-  if constexpr (N == 1) return __ldg(p);
-  else if constexpr (N == 2) return __ldg(reinterpret_cast<const uint16_t *>(p));
-  else return __ldg(reinterpret_cast<const uint32_t *>(p));
+template <int N> // 1, 2 or 4 bytes
+__device__ __forceinline__ uint32_t lds_bytes(uint32_t a) {
+  uint32_t w;
+  if constexpr (N == 1) asm volatile("ld.shared.u8 %0, [%1];" : "=r"(w) : "r"(a));
+  else if constexpr (N == 2) asm volatile("ld.shared.u16 %0, [%1];" : "=r"(w) : "r"(a));
+  else asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(a));
+  return w;
 }
 
-// The block-table row of a sequence, 32 entries at a time across the warp's lanes.
-struct TableWindow {
-  const int *row;
-  int maxp, base, entry;
-  __device__ __forceinline__ void start(const int *r, int n) {
-    row = r;
-    maxp = n;
-    base = -1;
-    entry = -1;
-  }
-  __device__ __forceinline__ int page(int p, int lane) { // p: the same in every lane
-    if ((p & ~31) != base) {
-      base = p & ~31;
-      entry = base + lane < maxp ? __ldg(row + base + lane) : -1;
-    }
-    return __shfl_sync(0xffffffffu, entry, p & 31);
+// Where a lane reads in a tile: its keys (row g; row g + 8 is 4 D bytes on), values (tokens 2 tig
+// and 2 tig + 1; those 8 on are 4 D bytes on) and scales. They go through a shuffle because the
+// compiler would otherwise compute them anew for every tile to save registers.
+template <int D>
+struct Reads {
+  uint32_t k, v[2], ks, vs;
+  __device__ __forceinline__ explicit Reads(int lane) {
+    const int g = lane >> 2, tig = lane & 3;
+    k = code_offset<D>(g, tig * (D / 8));
+    v[0] = 8 * D + code_offset<D>(2 * tig, g * (D / 16));
+    v[1] = 8 * D + code_offset<D>(2 * tig + 1, g * (D / 16));
+    ks = 16 * D + g * (D / 16) + tig * (D / 64);
+    vs = 17 * D + 2 * tig * (D / 16) + (D == 64 ? g / 2 : D == 128 ? g : 2 * g);
+    k = __shfl_sync(0xffffffffu, k, lane);
+    v[0] = __shfl_sync(0xffffffffu, v[0], lane);
+    v[1] = __shfl_sync(0xffffffffu, v[1], lane);
+    ks = __shfl_sync(0xffffffffu, ks, lane);
+    vs = __shfl_sync(0xffffffffu, vs, lane);
   }
 };
-
 template <int D>
-__device__ __forceinline__ void load_tile(const Kernel &k, TableWindow &win, int h, int tile, int lane, Tile<D> &t) {
-  const int g = lane >> 2, tig = lane & 3, pos = tile << 4;
-  const int page = win.page(pos >> k.c.pshift, lane);
-  t.mapped = page >= 0 && page < k.c.num_pages;
-  // records < 2^32 (the host checks), so the record index is one 32-bit word
-  const uint32_t rec = (((t.mapped ? page : 0) * static_cast<uint32_t>(k.c.Hkv) + h) << k.c.pshift) +
-                       (pos & ((1 << k.c.pshift) - 1));
-  const uint8_t *kc = k.c.codes[0] + static_cast<size_t>(rec) * (D / 2) + g * (D / 2) + tig * (D / 8);
-  const uint8_t *ks = k.c.scales[0] + static_cast<size_t>(rec) * (D / 16) + g * (D / 16) + tig * (D / 64);
-  const uint8_t *vc = k.c.codes[1] + static_cast<size_t>(rec) * (D / 2) + tig * D + g * (D / 16);
-  const uint8_t *vs = k.c.scales[1] + static_cast<size_t>(rec) * (D / 16) + tig * (D / 8) + g * D / 128;
+__device__ __forceinline__ void read_keys(uint32_t sm, const Reads<D> &at, Tile<D> &t) {
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
-    load_words(kc + r * 8 * (D / 2), t.k[r]);
-    t.ks[r] = load_scales<D / 64>(ks + r * 8 * (D / 16));
-  }
-#pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const int row = (s >> 1) * 8 + (s & 1);
-    load_words(vc + row * (D / 2), t.v[s]);
-    t.vs[s] = load_scales<(D == 256 ? 2 : 1)>(vs + row * (D / 16));
+    // the swizzle of rows 8 apart is the same; a lane's 32 bytes of D = 256 are two chunks of one XOR
+    lds(sm + at.k + r * 4 * D, t.k[r]);
+    t.ks[r] = lds_bytes<D / 64>(sm + at.ks + r * (D / 2));
   }
 }
+template <int D>
+__device__ __forceinline__ void read_values(uint32_t sm, const Reads<D> &at, Tile<D> &t) {
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    lds(sm + at.v[s & 1] + (s >> 1) * 4 * D, t.v[s]);
+    t.vs[s] = lds_bytes<(D == 256 ? 2 : 1)>(sm + at.vs + ((s >> 1) * 8 + (s & 1)) * (D / 16));
+  }
+}
+
+// A warp's way through its stretch of the weighted tile space: units one after the other. Positions
+// are relative to the stretch's begin.
+struct Cursor {
+  int b, nt, h, rb; // sequence, its tiles, KV head, row block
+  int at;           // position of the unit's first tile
+  __device__ __forceinline__ void start(const Kernel &k, int b0, uint32_t ahead) { // ahead: begin less b0's begin
+    b = b0;
+    nt = tiles_of(k, b);
+    const uint32_t unit = ahead / (nt + kUnitCost);
+    at = static_cast<int>(unit * (nt + kUnitCost) - ahead) + kUnitCost;
+    h = unit / k.row_blocks;
+    rb = unit - h * k.row_blocks;
+  }
+  __device__ __forceinline__ int first() const { return max(-at, 0); }
+  __device__ __forceinline__ int end(int len) const { return min(max(len - at, 0), nt); }
+  // the next unit that begins within the stretch; false at its end
+  __device__ __forceinline__ bool next(const Kernel &k, int len) {
+    at += nt + kUnitCost;
+    if (at - kUnitCost >= len) return false;
+    if (++rb < k.row_blocks) return true;
+    rb = 0;
+    if (++h < k.c.Hkv) return true;
+    h = 0;
+    do nt = tiles_of(k, ++b); // ends: the space below the stretch's end lies in some sequence
+    while (nt == 0);
+    return true;
+  }
+};
 
 // One warp's running state over its tiles.
 template <int D, int NT>
@@ -195,8 +255,8 @@ __device__ __forceinline__ void add_values(const Tile<D> &t, const uint32_t (&vs
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const uint32_t a = t.v[2 * u][w], b = t.v[2 * u + 1][w];
-      e2m1_to_h2((a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), even[u]);
-      e2m1_to_h2(((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u), odd[u]);
+      e2m1_to_h2(select_bits(a, b << 4), even[u]);
+      e2m1_to_h2(select_bits(a >> 4, b), odd[u]);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -218,157 +278,298 @@ __device__ __forceinline__ void add_values(const Tile<D> &t, const uint32_t (&vs
   }
 }
 
-// One tile. kMasked: some row of the block does not see every token of the tile (or its page is
-// unmapped); `limit` then holds the columns' position limits.
-template <int D, int NT, bool kMasked>
-__device__ __forceinline__ void do_tile(const Tile<D> &t, const uint32_t (&q)[NT][D / 8], const float (&mul)[NT][2],
-                                        const int (&limit)[NT][2], const Rows &rows, int row0, int G, int pos,
-                                        int lane, Acc<D, NT> &acc) {
-  const int g = lane >> 2, tig = lane & 3;
+// One tile. masked: some row of the block does not see every token of the tile, or its page is
+// unmapped.
+template <int D, int NT>
+__device__ __forceinline__ void do_tile(uint32_t sm, const Reads<D> &at, const uint32_t (&q)[NT][D / 8],
+                                        const float (&mul)[NT][2], const Kernel &k, int b, int row0, int pos,
+                                        bool mapped, bool masked, int lane, Acc<D, NT> &acc) {
+  Tile<D> t;
+  read_keys<D>(sm, at, t);
+  // the scales of the lane's D/64 blocks, as fp16 pairs
+  uint32_t scale2[2][(D + 64) / 128];
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int i = 0; i < (D + 64) / 128; ++i) scale2[r][i] = e4m3_to_h2(t.ks[r] >> (16 * i));
   float s[NT][4];
+#pragma unroll
+  for (int w = 0; w < D / 32; ++w) {
+    uint32_t c0[4], c1[4];
+    e2m1_to_h2(t.k[0][w], c0);
+    e2m1_to_h2(t.k[1][w], c1);
+    const uint32_t sel = w / 2 % 2 ? 0x3232u : 0x1010u; // the scale of this word's block, in both halves
+    const uint32_t s0 = prmt(scale2[0][w / 4], 0u, sel), s1 = prmt(scale2[1][w / 4], 0u, sel);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c0[j] = hmul2(c0[j], s0), c1[j] = hmul2(c1[j], s1);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (w == 0) mma16816_first(s[n], c0[0], c1[0], c0[1], c1[1], q[n][4 * w], q[n][4 * w + 1]);
+      else mma16816(s[n], c0[0], c1[0], c0[1], c1[1], q[n][4 * w], q[n][4 * w + 1]);
+      mma16816(s[n], c0[2], c1[2], c0[3], c1[3], q[n][4 * w + 2], q[n][4 * w + 3]);
+    }
+  }
+  read_values<D>(sm, at, t);
+  float x[NT][4]; // logits (log2 units) less the column's reference
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
+    for (int e = 0; e < 4; ++e) x[n][e] = fmaf(s[n][e], mul[n][e & 1], -acc.ref[n][e & 1]);
+  uint32_t p[NT][2];
+  auto weights = [&] { // softmax weights as the value MMAs take them; x = -infinity: not seen
+    float top = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < D / 32; ++w) {
-    uint32_t a[4], b[4];
-    e2m1_to_h2(t.k[0][w], a);
-    e2m1_to_h2(t.k[1][w], b);
-    // the scale of this word's block, in both halves
-    const uint32_t sel = (w / 2) * 0x11u;
-    const uint32_t sa = e4m3_to_h2(prmt(t.ks[0], 0u, sel | 0x4400u)), sb = e4m3_to_h2(prmt(t.ks[1], 0u, sel | 0x4400u));
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) a[j] = hmul2(a[j], sa), b[j] = hmul2(b[j], sb);
+      for (int e = 0; e < 4; ++e) top = fmaxf(top, x[n][e]);
+    if (__any_sync(0xffffffffu, top > kRefSlack)) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      mma16816(s[n], a[0], b[0], a[1], b[1], q[n][4 * w], q[n][4 * w + 1]);
-      mma16816(s[n], a[2], b[2], a[3], b[3], q[n][4 * w + 2], q[n][4 * w + 3]);
-    }
-  }
-  float x[NT][4]; // logits (log2 units) less the column's reference
-  bool move = false;
+      for (int n = 0; n < NT; ++n) {
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
+        for (int e = 0; e < 4; ++e) s[n][e] = x[n][e] == -INFINITY ? x[n][e] : s[n][e] * mul[n][e & 1];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      s[n][e] *= mul[n][e & 1];
-      if (kMasked && (pos + g + (e >> 1) * 8 >= limit[n][e & 1] || !t.mapped)) s[n][e] = -INFINITY;
-      x[n][e] = s[n][e] - acc.ref[n][e & 1];
-      move |= x[n][e] > kRefSlack;
-    }
-  }
-  if (__any_sync(0xffffffffu, move)) {
+        for (int c = 0; c < 2; ++c) {
+          float m = fmaxf(s[n][c], s[n][c + 2]);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+          for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          const float ref = fmaxf(acc.ref[n][c], m - kRefDrop), f = softmax_exp2(acc.ref[n][c] - ref);
+          acc.ref[n][c] = ref;
+          x[n][c] = s[n][c] - ref;
+          x[n][c + 2] = s[n][c + 2] - ref;
+          acc.l[n][c] *= f;
+          acc.l[n][c + 2] *= f;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float top = fmaxf(s[n][c], s[n][c + 2]);
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float ref = fmaxf(acc.ref[n][c], top - kRefDrop), f = softmax_exp2(acc.ref[n][c] - ref);
-        acc.ref[n][c] = ref;
-        x[n][c] = s[n][c] - ref;
-        x[n][c + 2] = s[n][c + 2] - ref;
-        acc.l[n][c] *= f;
-        acc.l[n][c + 2] *= f;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) acc.o[n][i][c] *= f, acc.o[n][i][c + 2] *= f;
+          for (int i = 0; i < D / 16; ++i) acc.o[n][i][c] *= f, acc.o[n][i][c + 2] *= f;
+        }
       }
     }
-  }
-  uint32_t p[NT][2];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    p[n][0] = transpose8x8(pack_h2(softmax_exp2(x[n][0]), softmax_exp2(x[n][1])));
-    p[n][1] = transpose8x8(pack_h2(softmax_exp2(x[n][2]), softmax_exp2(x[n][3])));
-    mma16816(acc.l[n], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, p[n][0], p[n][1]);
-  }
-  if constexpr (!kMasked) {
-    add_values<D, NT, false>(t, t.vs, p, acc);
-  } else {
+    for (int n = 0; n < NT; ++n) {
+      p[n][0] = transpose8x8(pack_h2(softmax_exp2(x[n][0]), softmax_exp2(x[n][1])));
+      p[n][1] = transpose8x8(pack_h2(softmax_exp2(x[n][2]), softmax_exp2(x[n][3])));
+      mma16816(acc.l[n], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, p[n][0], p[n][1]);
+    }
+  };
+  if (masked) {
+    const int g = lane >> 2, tig = lane & 3;
+    const Rows rows = rows_of(k, b);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int query = (row0 + 8 * n + 2 * tig + c) / k.G;
+        const int limit = !mapped ? 0 : query < rows.count ? rows.limit(query) : rows.seen;
+        if (pos + g >= limit) x[n][c] = -INFINITY;
+        if (pos + g + 8 >= limit) x[n][c + 2] = -INFINITY;
+      }
     // 0 * NaN is NaN: a token that a row does not see must not reach it through its scale either.
     // Tokens that no row sees get scale 0. A NaN scale among the rest of a masked tile is rare;
     // then each query of the block takes its own pass with only its own tokens and columns.
-    uint32_t vs[4];
     bool nan = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      vs[i] = pos + 2 * tig + (i >> 1) * 8 + (i & 1) < rows.seen && t.mapped ? t.vs[i] : 0u;
-      nan |= (vs[i] & 0x7Fu) == 0x7Fu || (vs[i] & 0x7F00u) == 0x7F00u;
+      if (!mapped || pos + 2 * tig + (i >> 1) * 8 + (i & 1) >= rows.seen) t.vs[i] = 0u;
+      nan |= (t.vs[i] & 0x7Fu) == 0x7Fu || (t.vs[i] & 0x7F00u) == 0x7F00u;
     }
-    if (!__any_sync(0xffffffffu, nan)) {
-      add_values<D, NT, false>(t, vs, p, acc);
-    } else {
-      const int last = min((row0 + 8 * NT - 1) / G, rows.count - 1);
-      for (int query = row0 / G; query <= last; ++query) {
+    if (__any_sync(0xffffffffu, nan)) {
+      weights();
+      const int last = min((row0 + 8 * NT - 1) / k.G, rows.count - 1);
+      for (int query = row0 / k.G; query <= last; ++query) {
         const int lim = rows.limit(query);
         uint32_t pq[NT][2], vq[4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const bool mine = (row0 + 8 * n + g) / G == query; // a fragment's column is row g
+          const bool mine = (row0 + 8 * n + g) / k.G == query; // a fragment's column is row g
           pq[n][0] = mine ? p[n][0] : 0u;
           pq[n][1] = mine ? p[n][1] : 0u;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) vq[i] = pos + 2 * tig + (i >> 1) * 8 + (i & 1) < lim ? vs[i] : 0u;
+        for (int i = 0; i < 4; ++i) vq[i] = pos + 2 * tig + (i >> 1) * 8 + (i & 1) < lim ? t.vs[i] : 0u;
         // columns of other queries still meet this pass's NaN scales, with weight 0
         unsigned own = 0;
 #pragma unroll
         for (int i = 0; i < 2 * NT; ++i)
-          own |= static_cast<unsigned>((row0 + 8 * (i >> 1) + 2 * tig + (i & 1)) / G == query) << i;
+          own |= static_cast<unsigned>((row0 + 8 * (i >> 1) + 2 * tig + (i & 1)) / k.G == query) << i;
         add_values<D, NT, true>(t, vq, pq, acc, own);
       }
+      return;
+    }
+  }
+  weights();
+  add_values<D, NT, false>(t, t.vs, p, acc);
+}
+
+constexpr int kCombineThreads = 256;
+// The weighted tile space (below 2^32: the host checks) over the warps of the CTAs that take part:
+// the first `more` shares are one longer than the others.
+struct Split {
+  uint32_t total, each, more;
+  __device__ __forceinline__ Split(uint32_t n, int ctas, int warps) {
+    total = n;
+    const uint32_t shares = min(static_cast<uint32_t>(ctas), max(n / (warps * kMinTiles), 1u)) * warps;
+    each = n / shares;
+    more = n - each * shares;
+  }
+  __device__ __forceinline__ uint32_t begin(uint32_t i) const { // shares behind the last one begin at the end
+    const uint64_t at = static_cast<uint64_t>(i) * each + min(i, more);
+    return at < total ? static_cast<uint32_t>(at) : total;
+  }
+  __device__ __forceinline__ uint32_t share_of(uint32_t at) const {
+    const uint32_t bend = more * (each + 1);
+    return at < bend ? at / (each + 1) : more + (at - bend) / each;
+  }
+};
+
+enum { kHead = 1, kHeadEnds = 2, kTail = 4, kSome = 8 }; // what a warp's stretch left behind
+
+// Writes a warp's state as a partial.
+template <int D, int NT>
+__device__ __forceinline__ void store_partial(float *slot, const Acc<D, NT> &acc, int lane) {
+  constexpr int R = 8 * NT;
+  const int g = lane >> 2, tig = lane & 3;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int r = 8 * n + 2 * tig + c;
+      if (g == 0) slot[R * D + 2 * r] = acc.ref[n][c], slot[R * D + 2 * r + 1] = acc.l[n][c];
+#pragma unroll
+      for (int i = 0; i < D / 16; i += 2)
+        *reinterpret_cast<float4 *>(slot + r * D + g * (D / 8) + 2 * i) =
+            make_float4(acc.o[n][i][c], acc.o[n][i][c + 2], acc.o[n][i + 1][c], acc.o[n][i + 1][c + 2]);
+    }
+}
+
+__device__ __forceinline__ long long out_row(const Kernel &k, int b, int h, int row) {
+  return (static_cast<long long>(b) * k.Lq + row / k.G) * k.Hq + h * k.G + row % k.G;
+}
+
+// Writes four elements of an output row from its sums. The largest weight is 2^11 or more: a sum of 0
+// means that every position was unmapped.
+template <int D>
+__device__ __forceinline__ void store_row(const Kernel &k, const Rows &rows, int b, int h, int row, int d, float l,
+                                          const float4 &o) {
+  const bool some = rows.limit(row / k.G) > 0 && l != 0.0f;
+  const float inv = k.c.g[1] / l;
+  const long long at = out_row(k, b, h, row) * D + d;
+  store_out(k, at, some ? o.x * inv : 0.0f, some ? o.y * inv : 0.0f);
+  store_out(k, at + 2, some ? o.z * inv : 0.0f, some ? o.w * inv : 0.0f);
+}
+
+// Writes a unit that one warp has seen whole.
+template <int D, int NT>
+__device__ __forceinline__ void store_whole(const Kernel &k, const Rows &rows, int b, int h, int row0,
+                                            const Acc<D, NT> &acc, int lane) {
+  const int g = lane >> 2, tig = lane & 3;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int row = row0 + 8 * n + 2 * tig + c;
+      if (row >= k.Lq * k.G) continue;
+      const bool some = rows.limit(row / k.G) > 0 && acc.l[n][c] != 0.0f; // as in store_row
+      const float inv = k.c.g[1] / acc.l[n][c];
+      float x[D / 8];
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        x[2 * i] = some ? acc.o[n][i][c] * inv : 0.0f;
+        x[2 * i + 1] = some ? acc.o[n][i][c + 2] * inv : 0.0f;
+      }
+      store_vec<D / 8>(k.out, k.out_dtype, static_cast<size_t>(out_row(k, b, h, row) * D + g * (D / 8)), x);
+    }
+}
+
+// Queries of a unit: row g of each column tile as fp16, and what turns the columns' scores into log2
+// units. fp16 queries are taken as they are; bf16 rows are multiplied by the power of two that brings
+// their largest element to 2^14..2^15 (2^126 at most: bf16 values are multiples of 2^-133).
+template <int D, int NT>
+__device__ __forceinline__ void load_queries(const Kernel &k, const Rows &rows, int b, int h, int row0, int lane,
+                                             uint32_t (&q)[NT][D / 8], float (&mul)[NT][2]) {
+  const int g = lane >> 2, tig = lane & 3;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int row = row0 + 8 * n + g;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) q[n][i] = 0u;
+    if (row / k.G < rows.count) {
+      const uint4 *src = reinterpret_cast<const uint4 *>(k.q + out_row(k, b, h, row) * D + tig * (D / 4));
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint4 v = __ldg(src + i);
+        q[n][4 * i] = v.x, q[n][4 * i + 1] = v.y, q[n][4 * i + 2] = v.z, q[n][4 * i + 3] = v.w;
+      }
+    }
+    int e = 0;
+    if (k.bf16) {
+      uint32_t top = 0; // the largest magnitude in each half, as bits; infinities and NaN stand above
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) top = __vmaxu2(top, q[n][i] & 0x7FFF7FFFu);
+      top = max(top >> 16, top & 0xFFFFu);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int field = top >> 7; // of the exponent
+      e = top == 0 || field == 255 ? 0 : min(141 - field, 126);
+      const float f = __uint_as_float((127 + e) << 23);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) q[n][i] = pack_h2(bf16_lo(q[n][i]) * f, bf16_hi(q[n][i]) * f);
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int ec = __shfl_sync(0xffffffffu, e, (2 * tig + c) * 4);
+      mul[n][c] = k.scale * __uint_as_float((127 - ec) << 23) * k.klog;
     }
   }
 }
 
 template <int D, int NT>
-constexpr int smem_bytes() {
-  return kWarps * 8 * NT * (D + 4) * 4 + kWarps * 8 * NT * 2 * 4;
-}
-
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, D == 256 || NT > 1 ? 1 : 2) mx_decode_kernel(const Kernel k) {
-  constexpr int R = 8 * NT;   // rows of a block
-  constexpr int kP = D + 4;   // padded row of the merge buffer
-  extern __shared__ float sm[];
-  float *so = sm, *sr = sm + kWarps * R * kP; // [warp][R][kP]; [warp][R]{reference, sum}
-  __shared__ long long s_scan[kWarps];
-  __shared__ long long s_start;
-  __shared__ int s_b0;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tig = lane & 3;
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) mx_decode_kernel(const Kernel k) {
+  using C = Cfg<D, NT>;
+  constexpr int R = 8 * NT, W = kWarps, S = C::kStages;
+  extern __shared__ __align__(128) uint8_t sm[];
+  __shared__ uint32_t s_scan[W], s_bound[W + 1], s_ahead[W];
+  __shared__ int s_b0[W], s_left[W];
+  __shared__ int4 s_tail[W];
+  __shared__ Rows s_rows[W]; // of the tails
+  __shared__ Cursor s_copy[W], s_done[W]; // where the warps' copies and sums are (out of the registers' way)
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
-  // ---- this CTA's stretch of the flattened tile space
+  // ---- the warps' stretches of the weighted tile space
   const int B = k.c.B, per = (B + kThreads - 1) / kThreads;
-  const long long heads = static_cast<long long>(k.c.Hkv) * k.row_blocks;
-  long long mine = 0;
+  const int units = k.c.Hkv * k.row_blocks; // of a sequence
+  uint32_t mine = 0;
   for (int i = 0; i < per; ++i)
-    if (tid * per + i < B) mine += tiles_of(k, tid * per + i);
-  long long incl = mine;
+    if (tid * per + i < B) {
+      const int nt = tiles_of(k, tid * per + i);
+      mine += nt ? (nt + kUnitCost) * units : 0;
+    }
+  uint32_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
   if (lane == 31) s_scan[warp] = incl;
   __syncthreads();
-  long long before = 0, total = 0;
+  uint32_t before = 0, total = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < W; ++w) {
     if (w < warp) before += s_scan[w];
     total += s_scan[w];
   }
-  total *= heads;
-  const long long n = min(static_cast<long long>(gridDim.x), max(total / kMinTiles, 1ll));
   const int cta = blockIdx.x;
-  const long long lo = cta < n ? total * cta / n : total, hi = cta < n ? total * (cta + 1) / n : total;
-  long long at = (before + incl - mine) * heads;
+  const Split split(total, gridDim.x, W);
+  if (tid <= W) s_bound[tid] = split.begin(cta * W + tid);
+  __syncthreads();
+  uint32_t at = before + incl - mine;
   for (int i = 0; i < per; ++i) {
     const int b = tid * per + i;
     if (b >= B) break;
-    const long long len = tiles_of(k, b) * heads;
-    if (lo >= at && lo < at + len) s_b0 = b, s_start = at;
+    const int nt = tiles_of(k, b);
+    if (nt == 0) continue;
+    const uint32_t len = (nt + kUnitCost) * units;
+    if (at <= s_bound[W - 1] && at + (len - 1) >= s_bound[0])
+      for (int w = 0; w < W; ++w)
+        if (s_bound[w] >= at && s_bound[w] - at < len) s_b0[w] = b, s_ahead[w] = s_bound[w] - at;
     at += len;
   }
   // sequences without tiles have only empty rows
@@ -379,206 +580,291 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT > 1 ? 1 : 2) mx_decod
       store_out(k, base + i, 0.0f, 0.0f);
   }
   __syncthreads();
-  if (lo >= hi) {
-    if (tid == 0) k.desc[cta] = make_int4(0, 0, 0, 0);
-    return;
-  }
-  int b = s_b0;
-  long long start = s_start, cur = lo; // first tile of sequence b, and of this stretch
-  int4 desc = make_int4(0, 0, 0, 0);
-  while (cur < hi) {
-    int nt_b = tiles_of(k, b);
-    while (cur >= start + nt_b * heads) { // next sequence that has tiles
-      start += nt_b * heads;
-      nt_b = tiles_of(k, ++b);
-    }
-    const long long unit = (cur - start) / nt_b, unit0 = start + unit * nt_b;
-    const int h = static_cast<int>(unit / k.row_blocks), rb = static_cast<int>(unit - static_cast<long long>(h) * k.row_blocks);
-    const int t0 = static_cast<int>(cur - unit0), t1 = static_cast<int>(min(static_cast<long long>(nt_b), hi - unit0));
-    const Rows rows = rows_of(k, b);
-    const int row0 = rb * R;
-    // ---- queries: row g of each column tile, scaled by a power of two into fp16
-    uint32_t q[NT][D / 8];
-    float mul[NT][2];
-    int limit[NT][2];
-    int full = rows.seen; // every row of the block sees the positions below
-#pragma unroll
-    for (int n_ = 0; n_ < NT; ++n_) {
-      const int row = row0 + 8 * n_ + g, query = row / k.G;
-      float x[D / 4];
-      float top = 0.0f;
-      if (query < rows.count) {
-        const uint16_t *src = k.q + ((static_cast<long long>(b) * k.Lq + query) * k.Hq + h * k.G + row % k.G) * D + tig * (D / 4);
-        if (k.bf16) load_vec<D / 4>(src, TQ_BF16, 0, x);
-        else load_vec<D / 4>(src, TQ_F16, 0, x);
-      } else {
-#pragma unroll
-        for (int i = 0; i < D / 4; ++i) x[i] = 0.0f;
+  const int len = static_cast<int>(s_bound[warp + 1] - s_bound[warp]);
+  uint8_t *ring = sm + warp * C::kWarpBytes;
+  int left = 0;
+  if (len > 0) {
+    const uint32_t ring_addr = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+    // ---- copies run S - 1 tiles ahead; `run` tiles, from record rec, are left on the current page
+    // the lane's 16 bytes of the next tile: `chunk` in the codes, `schunk` in the scales (keys' in the first
+    // half of D/8 lanes, values' in the second; further lanes repeat them)
+    const uint8_t *sc = k.c.scales[lane / (D / 16) & 1];
+    const uint32_t swz = __shfl_sync(0xffffffffu, (lane >> 3) * 128 + (((lane & 7) ^ chunk_swizzle<D>(lane >> 3)) << 4), lane);
+    const uint32_t sdst = __shfl_sync(0xffffffffu, 16 * D + (lane & (D / 8 - 1)) * 16, lane);
+    uint32_t chunk = 0, schunk = 0;
+    const int page_tiles = 1 << (k.c.pshift - 4);
+    const int *entry;            // table entry behind next_page's
+    int run, left_tiles;         // tiles left on the current page, and of the unit's behind it
+    int next_page;               // the page behind the current one, read ahead
+    uint32_t head;               // first record of the head in page 0
+    unsigned mapped = 0, ok;     // a bit for each copied tile, the latest lowest; the current page's
+    // Unmapped pages, and what is behind the stretch's end, copy records of page 0: never looked at, and
+    // cheaper than a branch for every tile.
+    auto enter_page = [&](int in_page) {
+      ok = static_cast<unsigned>(next_page) < static_cast<unsigned>(k.c.num_pages);
+      // 16-byte chunks of codes < 2^32 (the host checks), so their index is one 32-bit word
+      const uint32_t rec = ok ? ((next_page * static_cast<uint32_t>(k.c.Hkv)) << k.c.pshift) + head + (in_page << 4) : 0u;
+      chunk = rec * (D / 32) + lane;
+      schunk = (rec >> 4) * (D / 16) + (lane & (D / 16 - 1));
+      run = page_tiles - in_page;
+      if (left_tiles > 0) {
+        run = min(run, left_tiles);
+        left_tiles -= run;
+        if (left_tiles > 0) next_page = __ldg(entry++);
       }
-#pragma unroll
-      for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(x[i]));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // exponent that brings the largest element to 2^14..2^15; a row of zeros, infinities or NaN
-      // keeps its values
-      const int e = top > 0.0f && top < INFINITY ? 14 - ilogbf(top) : 0;
-      const float f1 = ldexpf(1.0f, e / 2), f2_ = ldexpf(1.0f, e - e / 2);
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) q[n_][i] = pack_h2(x[2 * i] * f1 * f2_, x[2 * i + 1] * f1 * f2_);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int ec = __shfl_sync(0xffffffffu, e, (2 * tig + c) * 4);
-        mul[n_][c] = ldexpf(k.scale, -ec) * k.klog;
-        const int qc = (row0 + 8 * n_ + 2 * tig + c) / k.G;
-        limit[n_][c] = qc < rows.count ? rows.limit(qc) : rows.seen;
+    };
+    {
+      Cursor c;
+      c.start(k, s_b0[warp], s_ahead[warp]);
+      s_done[warp] = s_copy[warp] = c;
+      const int tile = c.first();
+      left_tiles = max(c.end(len) - tile, 0); // 0: the stretch begins with the cost of a unit
+      entry = k.c.bt + static_cast<long long>(c.b) * k.c.maxp + (tile >> (k.c.pshift - 4));
+      head = static_cast<uint32_t>(c.h) << k.c.pshift;
+      run = 0;
+      if (left_tiles > 0) {
+        next_page = __ldg(entry++);
+        enter_page(tile & (page_tiles - 1));
       }
     }
-    if (row0 / k.G < rows.count) full = rows.limit(row0 / k.G);
-    // ---- the warp's tiles
-    Acc<D, NT> acc;
-#pragma unroll
-    for (int n_ = 0; n_ < NT; ++n_) {
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc.o[n_][i][e] = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc.l[n_][e] = 0.0f;
-      acc.ref[n_][0] = acc.ref[n_][1] = kRefEmpty;
-    }
-    const int share = (t1 - t0 + kWarps - 1) / kWarps;
-    const int w0 = min(t0 + warp * share, t1), w1 = min(w0 + share, t1);
-    if (w0 < w1) {
-      TableWindow win;
-      win.start(k.c.bt + static_cast<long long>(b) * k.c.maxp, k.c.maxp);
-      Tile<D> cur_t, next_t;
-      load_tile<D>(k, win, h, w0, lane, cur_t);
-      for (int tile = w0; tile < w1; ++tile) {
-        if (tile + 1 < w1) load_tile<D>(k, win, h, tile + 1, lane, next_t);
-        const int pos = tile << 4;
-        if (pos + 16 <= full && cur_t.mapped)
-          do_tile<D, NT, false>(cur_t, q, mul, limit, rows, row0, k.G, pos, lane, acc);
-        else
-          do_tile<D, NT, true>(cur_t, q, mul, limit, rows, row0, k.G, pos, lane, acc);
-        cur_t = next_t;
-      }
-    }
-    // ---- merge the warps
-    __syncthreads(); // the buffer's readers of the stretch before are done
-#pragma unroll
-    for (int n_ = 0; n_ < NT; ++n_)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int r = 8 * n_ + 2 * tig + c;
-        if (g == 0) {
-          sr[(warp * R + r) * 2] = acc.ref[n_][c];
-          sr[(warp * R + r) * 2 + 1] = acc.l[n_][c];
+    __syncwarp();
+    auto copy_tile = [&](uint32_t dst) {
+      if (run == 0) {
+        if (left_tiles == 0) { // the next unit with tiles in the stretch
+          Cursor c = s_copy[warp];
+          bool more;
+          do more = c.next(k, len);
+          while (more && c.end(len) == 0);
+          next_page = -1;
+          if (more) {
+            left_tiles = c.end(len);
+            entry = k.c.bt + static_cast<long long>(c.b) * k.c.maxp;
+            head = static_cast<uint32_t>(c.h) << k.c.pshift;
+            next_page = __ldg(entry++);
+          }
+          __syncwarp();
+          s_copy[warp] = c;
+          __syncwarp();
         }
+        enter_page(0);
+      }
+      const uint8_t *a = k.c.codes[0] + static_cast<size_t>(chunk) * 16, *b = k.c.codes[1] + static_cast<size_t>(chunk) * 16;
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) { // 512 bytes: the swizzle of lines 4 apart differs for D = 256 only
+        const uint32_t to = dst + (D == 256 ? swz ^ ((j & 1) << 6) : swz) + j * 512;
+        copy16(to, a + j * 512);
+        copy16(to + 8 * D, b + j * 512);
+      }
+      copy16(dst + sdst, sc + static_cast<size_t>(schunk) * 16);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      chunk += D / 2;
+      schunk += D / 16;
+      --run;
+      mapped = 2 * mapped + ok;
+    };
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) copy_tile(ring_addr + i * C::kTile);
+    const Reads<D> reads(lane);
+    int at_stage = 0, free_stage = (S - 1) * C::kTile; // byte offsets of the next tile and of the next copy
+    left = kSome;
+    bool more;
+    do {
+      const Cursor cu = s_done[warp];
+      const int t0 = cu.first(), t1 = cu.end(len);
+      if (t0 < t1) {
+      const int b = cu.b, h = cu.h, row0 = cu.rb * R;
+      uint32_t q[NT][D / 8];
+      float mul[NT][2];
+      int full; // every row of the block sees the positions below
+      {
+        const Rows rows = rows_of(k, b);
+        load_queries<D, NT>(k, rows, b, h, row0, lane, q, mul);
+        full = row0 / k.G < rows.count ? rows.limit(row0 / k.G) : rows.seen;
+      }
+      Acc<D, NT> acc;
+#pragma unroll
+      for (int n_ = 0; n_ < NT; ++n_) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-          *reinterpret_cast<float2 *>(so + (warp * R + r) * kP + g * (D / 8) + 2 * i) =
-              make_float2(acc.o[n_][i][c], acc.o[n_][i][c + 2]);
-      }
-    __syncthreads();
-    const bool whole = t0 == 0 && t1 == nt_b;
-    float *slot = k.part + static_cast<long long>(2 * cta + (t0 == 0 ? 1 : 0)) * R * (D + 2);
-    for (int i = tid; i < R * (D / 2); i += kThreads) {
-      const int r = i / (D / 2), d = 2 * (i - r * (D / 2));
-      float ref = kRefEmpty, l = 0.0f, o0 = 0.0f, o1 = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) ref = fmaxf(ref, sr[(w * R + r) * 2]);
+          for (int e = 0; e < 4; ++e) acc.o[n_][i][e] = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = softmax_exp2(sr[(w * R + r) * 2] - ref);
-        const float2 v = *reinterpret_cast<const float2 *>(so + (w * R + r) * kP + d);
-        l += f * sr[(w * R + r) * 2 + 1];
-        o0 += f * v.x;
-        o1 += f * v.y;
+        for (int e = 0; e < 4; ++e) acc.l[n_][e] = 0.0f;
+        acc.ref[n_][0] = acc.ref[n_][1] = kRefEmpty;
       }
-      if (whole) {
-        const int query = (row0 + r) / k.G;
-        if (query < k.Lq) {
-          // the largest weight is 2^11 or more: a sum of 0 means that every position was unmapped
-          const bool some = rows.limit(query) > 0 && l != 0.0f;
-          const float inv = k.c.g[1] / l;
-          store_out(k, ((static_cast<long long>(b) * k.Lq + query) * k.Hq + h * k.G + (row0 + r) % k.G) * D + d,
-                    some ? o0 * inv : 0.0f, some ? o1 * inv : 0.0f);
+      for (int tile = t0; tile < t1; ++tile) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+        __syncwarp(); // all lanes' copies of this tile are there, and the oldest stage's readers are done
+        copy_tile(ring_addr + free_stage);
+        const bool here = mapped >> (S - 1) & 1u;
+        const int pos = tile << 4;
+        do_tile<D, NT>(ring_addr + at_stage, reads, q, mul, k, b, row0, pos, here, pos + 16 > full || !here, lane, acc);
+        free_stage = at_stage;
+        at_stage = at_stage + C::kTile == S * C::kTile ? 0 : at_stage + C::kTile;
+      }
+      if (t0 > 0) {
+        left |= kHead | (t1 == cu.nt ? kHeadEnds : 0);
+        store_partial<D, NT>(reinterpret_cast<float *>(ring + S * C::kTile), acc, lane);
+      } else if (t1 == cu.nt) {
+        store_whole<D, NT>(k, rows_of(k, b), b, h, row0, acc, lane);
+      } else { // the last unit of the stretch: its partial takes the ring's place
+        left |= kTail;
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncwarp();
+        store_partial<D, NT>(reinterpret_cast<float *>(ring), acc, lane);
+        if (lane == 0) {
+          const uint32_t last = s_bound[warp] + cu.at + cu.nt - 1; // the unit's last tile, in the whole space
+          s_tail[warp] = make_int4(b, h, row0, static_cast<int>(split.share_of(last) / W) - cta + 1);
+          s_rows[warp] = rows_of(k, b);
         }
+      }
+      }
+      Cursor c = s_done[warp];
+      more = c.next(k, len);
+      __syncwarp();
+      s_done[warp] = c;
+      __syncwarp();
+    } while (more);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  }
+  pdl_trigger();
+  if (lane == 0) s_left[warp] = left;
+  __syncthreads();
+  // ---- join the warps' partials: a cut unit is the tail of one warp and the heads of those behind it
+  unsigned some = 0, heads = 0, ends = 0, tails = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    const int l = s_left[w];
+    some |= (l & kSome ? 1u : 0u) << w, heads |= (l & kHead ? 1u : 0u) << w;
+    ends |= (l & kHeadEnds ? 1u : 0u) << w, tails |= (l & kTail ? 1u : 0u) << w;
+  }
+  constexpr int kPer = 4; // adjacent elements of a row that a thread joins at a time
+  bool goes_on = false;
+#pragma unroll 1
+  for (int first = -1; first < W; ++first) { // -1: the unit that CTAs before this one began
+    if (first >= 0 && !(tails >> first & 1u)) continue;
+    // the heads behind: up to the first that ends the unit, or before the first warp that begins with another
+    const unsigned behind = ~0u << (first + 1);
+    const unsigned stop = behind & (ends | (some & ~heads));
+    unsigned parts = heads & behind & (stop ? (stop & ~(stop - 1)) * 2 - 1 : ~0u);
+    if (first < 0 && parts == 0) continue;
+    const bool whole = first >= 0 && (parts & ends);
+    goes_on |= first >= 0 && !whole;
+    if (first >= 0) parts |= 1u << first;
+    if (first >= 0 && !whole && tid == 0) k.desc[cta] = s_tail[first];
+    float *dst = k.part + (2ll * cta + (first >= 0)) * (C::kSlot / 4);
+#pragma unroll 1
+    for (int i = tid * kPer; i < R * D; i += kThreads * kPer) {
+      const int r = i / D;
+      const float *src[W];
+      float2 st[W]; // references and sums
+      float ref = kRefEmpty;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        src[w] = reinterpret_cast<const float *>(sm + w * C::kWarpBytes + (w == first ? 0 : S * C::kTile));
+        st[w] = parts >> w & 1u ? *reinterpret_cast<const float2 *>(src[w] + R * D + 2 * r) : make_float2(kRefEmpty, 0.0f);
+        ref = fmaxf(ref, st[w].x);
+      }
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float l = 0.0f;
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+        if (parts >> w & 1u) {
+          const float f = softmax_exp2(st[w].x - ref);
+          const float4 v = *reinterpret_cast<const float4 *>(src[w] + i);
+          l = fmaf(f, st[w].y, l);
+          o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y), o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+        }
+      if (whole) {
+        const int row = s_tail[first].z + r;
+        if (row >= k.Lq * k.G) continue;
+        store_row<D>(k, s_rows[first], s_tail[first].x, s_tail[first].y, row, i % D, l, o);
       } else {
-        *reinterpret_cast<float2 *>(slot + r * D + d) = make_float2(o0, o1);
-        if (d == 0) slot[R * D + 2 * r] = ref, slot[R * D + 2 * r + 1] = l;
+        *reinterpret_cast<float4 *>(dst + i) = o;
+        if (i % D == 0) *reinterpret_cast<float2 *>(dst + R * D + 2 * r) = make_float2(ref, l);
       }
     }
-    if (!whole && t0 == 0) { // the unit goes on in the CTAs behind: this one describes it
-      const long long end = unit0 + nt_b;
-      const int last = static_cast<int>((end * n - 1) / total);
-      desc = make_int4(b, h, rb, last - cta + 1);
-    }
-    cur = unit0 + t1;
   }
-  if (tid == 0) k.desc[cta] = desc;
+  if (tid == 0 && !goes_on) k.desc[cta] = make_int4(0, 0, 0, 0);
 }
 
 // Joins the partials of a unit that several CTAs share: parts 0 (slot 1 of its first CTA) and
 // 1.. (slot 0 of the CTAs behind it). One CTA for each boundary; most return at once.
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads) mx_combine_kernel(const Kernel k) {
-  constexpr int R = 8 * NT;
+__global__ void __launch_bounds__(kCombineThreads) mx_combine_kernel(const Kernel k) {
+  constexpr int R = 8 * NT, kSlot = Cfg<D, NT>::kSlot / 4;
   pdl_wait();
   const int cta = blockIdx.x;
   const int4 d = k.desc[cta];
   if (d.w == 0) return;
-  const int b = d.x, h = d.y, row0 = d.z * R, parts = d.w;
-  const Rows rows = rows_of(k, b);
-  const long long stride = static_cast<long long>(R) * (D + 2);
-  const float *first = k.part + (2ll * cta + 1) * stride, *rest = k.part + 2ll * (cta + 1) * stride;
-  for (int i = threadIdx.x; i < R * (D / 2); i += kThreads) {
-    const int r = i / (D / 2), e = 2 * (i - r * (D / 2));
-    const int query = (row0 + r) / k.G;
-    if (query >= k.Lq) continue;
-    float o0 = 0.0f, o1 = 0.0f, l = 0.0f;
-    const bool some = rows.limit(query) > 0;
-    if (some) {
-      float ref = first[R * D + 2 * r];
-      for (int p = 0; p + 1 < parts; ++p) ref = fmaxf(ref, rest[2 * p * stride + R * D + 2 * r]);
+  const int parts = d.w;
+  const Rows rows = rows_of(k, d.x);
+  const float *first = k.part + (2ll * cta + 1) * kSlot, *rest = k.part + 2ll * cta * kSlot; // part p > 0: rest + 2 p slots
+#pragma unroll 1
+  for (int i = threadIdx.x * 4; i < R * D; i += kCombineThreads * 4) {
+    const int r = i / D;
+    if (d.z + r >= k.Lq * k.G) break;
+    float2 st = *reinterpret_cast<const float2 *>(first + R * D + 2 * r);
+    float4 o = *reinterpret_cast<const float4 *>(first + i);
+    float ref = st.x, l = st.y;
 #pragma unroll 4
-      for (int p = 0; p < parts; ++p) {
-        const float *s = p == 0 ? first : rest + 2 * (p - 1) * stride;
-        const float f = softmax_exp2(s[R * D + 2 * r] - ref);
-        const float2 v = *reinterpret_cast<const float2 *>(s + r * D + e);
-        l += f * s[R * D + 2 * r + 1];
-        o0 += f * v.x;
-        o1 += f * v.y;
-      }
-      const float inv = l != 0.0f ? k.c.g[1] / l : 0.0f; // as above
-      o0 *= inv;
-      o1 *= inv;
+    for (int p = 1; p < parts; ++p) { // the first part's sums are scaled along
+      const float *s = rest + 2ll * p * kSlot;
+      st = *reinterpret_cast<const float2 *>(s + R * D + 2 * r);
+      const float4 v = *reinterpret_cast<const float4 *>(s + i);
+      const float now = fmaxf(ref, st.x), back = softmax_exp2(ref - now), f = softmax_exp2(st.x - now);
+      ref = now;
+      l = fmaf(f, st.y, l * back);
+      o.x = fmaf(f, v.x, o.x * back), o.y = fmaf(f, v.y, o.y * back);
+      o.z = fmaf(f, v.z, o.z * back), o.w = fmaf(f, v.w, o.w * back);
     }
-    store_out(k, ((static_cast<long long>(b) * k.Lq + query) * k.Hq + h * k.G + (row0 + r) % k.G) * D + e, o0, o1);
+    store_row<D>(k, rows, d.x, d.y, d.z + r, i % D, l, o);
   }
 }
 
 template <int D, int NT>
 cudaError_t run(const Kernel &k, const MxPlan &p, cudaStream_t s) {
-  constexpr int smem = smem_bytes<D, NT>();
+  constexpr int smem = Cfg<D, NT>::kSmem;
   cudaError_t e = cudaFuncSetAttribute(mx_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(mx_decode_kernel<D, NT>, dim3(p.ctas), dim3(kThreads), smem, s, k);
   if (e != cudaSuccess) return e;
-  return launch_pdl(mx_combine_kernel<D, NT>, dim3(p.ctas), dim3(kThreads), 0, s, k);
+  return launch_pdl(mx_combine_kernel<D, NT>, dim3(p.ctas), dim3(kCombineThreads), 0, s, k);
 }
+
+template <class F>
+auto with_shape(int d, int nt, F &&f) { // f.operator()<D, NT>()
+  if (d == 64) return nt == 1 ? f.template operator()<64, 1>() : nt == 2 ? f.template operator()<64, 2>() : f.template operator()<64, 3>();
+  if (d == 128) return nt == 1 ? f.template operator()<128, 1>() : nt == 2 ? f.template operator()<128, 2>() : f.template operator()<128, 3>();
+  return f.template operator()<256, 1>();
+}
+
+struct Ctas { // of an SM
+  template <int D, int NT>
+  int operator()() const { return Cfg<D, NT>::kCtas; }
+};
+struct Launch {
+  const Kernel &k;
+  const MxPlan &p;
+  cudaStream_t s;
+  template <int D, int NT>
+  cudaError_t operator()() const { return run<D, NT>(k, p, s); }
+};
 
 } // namespace
 
 MxPlan plan_mx_decode(int Hkv, int d, int Hq, int Lq, int sm_count) {
   MxPlan p;
-  const int rows = Lq * (Hq / Hkv);
-  p.nt = d < 256 && rows > 8 ? 2 : 1;
-  p.row_blocks = (rows + 8 * p.nt - 1) / (8 * p.nt);
-  p.ctas = sm_count * (d == 256 || p.nt > 1 ? 1 : 2);
-  // partials of one launch: 2 ctas x 8 nt rows, the same for both tile counts; one descriptor per
-  // CTA, at most two CTAs an SM. One size serves every number of queries and heads.
-  p.ws_bytes = static_cast<size_t>(4) * sm_count * 8 * (d + 2) * sizeof(float) + 2 * sm_count * sizeof(int4);
+  const int rows = Lq * (Hq / Hkv), most = d == 256 ? 1 : 3;
+  p.row_blocks = (rows + 8 * most - 1) / (8 * most);
+  p.nt = (rows + 8 * p.row_blocks - 1) / (8 * p.row_blocks);
+  p.ctas = sm_count * with_shape(d, p.nt, Ctas{});
+  // one size serves every number of queries and heads: the largest of the tile counts'
+  p.ws_bytes = 0;
+  for (int nt = 1; nt <= most; ++nt) {
+    const size_t ctas = static_cast<size_t>(sm_count) * with_shape(d, nt, Ctas{});
+    p.ws_bytes = std::max(p.ws_bytes, ctas * (2 * 8 * nt * (d + 2) * sizeof(float) + sizeof(int4)));
+  }
   return p;
 }
 
@@ -599,9 +885,7 @@ cudaError_t launch_mx_decode(const MxDecodeArgs &a, cudaStream_t s) {
   k.out_dtype = a.out_dtype;
   k.scale = a.scale;
   k.klog = 1.4426950408889634f * a.c.g[0];
-  if (a.c.d == 64) return a.plan.nt == 1 ? run<64, 1>(k, a.plan, s) : run<64, 2>(k, a.plan, s);
-  if (a.c.d == 128) return a.plan.nt == 1 ? run<128, 1>(k, a.plan, s) : run<128, 2>(k, a.plan, s);
-  return run<256, 1>(k, a.plan, s);
+  return with_shape(a.c.d, a.plan.nt, Launch{k, a.plan, s});
 }
 
 } // namespace tq
