@@ -47,13 +47,17 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 template <int D, int NT>
 struct Cfg {
-  static constexpr int kCtas = D == 64 && NT == 1 ? 4 : D == 256 || (D == 128 && NT == 3) ? 2 : 3;
-  static constexpr int kStages = D == 64 || (D == 128 && NT == 3) ? 6 : 4;
+  static constexpr int kCtas = D == 64 && NT == 1 ? 4 : D == 256 || (D == 128 && NT > 1) ? 2 : 3;
+  static constexpr bool kQueriesInSmem = NT > 1;       // the registers hold NT times the sums
+  static constexpr int kStages = D == 64 ? 6 : 4;
   static constexpr int kTile = 18 * D;                 // bytes: 16 x (D/2 + D/16) of keys and of values
   static constexpr int kSlot = 8 * NT * (D + 2) * 4;   // bytes of a partial: sums, then (reference, weight sum)
-  static constexpr int kWarpBytes = kStages * kTile + kSlot;
+  static constexpr int kQueries = kQueriesInSmem ? 16 * D * NT : 0;
+  static constexpr int kWarpBytes = kStages * kTile + kSlot + kQueries;
   static constexpr int kSmem = kWarps * kWarpBytes;
-  static_assert(kSlot <= kStages * kTile && kTile % 16 == 0 && kSlot % 16 == 0, "the tail's partial reuses the ring");
+  static_assert(kCtas * (kSmem + 2048) <= 228 * 1024, "the CTAs of an SM are resident together");
+  static constexpr int kHeadAt = kStages * kTile + kQueries; // of the slot for the stretch's first unit
+  static_assert(kSlot <= kHeadAt && kTile % 16 == 0 && kSlot % 16 == 0, "the tail's partial reuses ring and queries");
 };
 
 struct Kernel {
@@ -278,10 +282,38 @@ __device__ __forceinline__ void add_values(const Tile<D> &t, const uint32_t (&vs
   }
 }
 
+// A unit's queries as the score MMAs take them: four registers for 32 elements of 8 rows, held in
+// registers or (kQueriesInSmem) in the warp's shared memory, 16 bytes a lane.
+template <int D, int NT, bool kSmem = Cfg<D, NT>::kQueriesInSmem>
+struct Queries {
+  uint32_t f[NT][D / 8];
+  __device__ __forceinline__ void bind(uint32_t) {}
+  __device__ __forceinline__ void put(int n, const uint32_t (&x)[D / 8]) {
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) f[n][i] = x[i];
+  }
+  __device__ __forceinline__ void get(int n, int w, uint32_t (&x)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = f[n][4 * w + i];
+  }
+};
+template <int D, int NT>
+struct Queries<D, NT, true> {
+  uint32_t at; // the lane's
+  __device__ __forceinline__ void bind(uint32_t a) { at = a; }
+  __device__ __forceinline__ void put(int n, const uint32_t (&x)[D / 8]) {
+#pragma unroll
+    for (int i = 0; i < D / 8; i += 4)
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + (n * (D / 32) + i / 4) * 512), "r"(x[i]),
+                   "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3]));
+  }
+  __device__ __forceinline__ void get(int n, int w, uint32_t (&x)[4]) const { lds(at + (n * (D / 32) + w) * 512, x); }
+};
+
 // One tile. masked: some row of the block does not see every token of the tile, or its page is
 // unmapped.
 template <int D, int NT>
-__device__ __forceinline__ void do_tile(uint32_t sm, const Reads<D> &at, const uint32_t (&q)[NT][D / 8],
+__device__ __forceinline__ void do_tile(uint32_t sm, const Reads<D> &at, const Queries<D, NT> &q,
                                         const float (&mul)[NT][2], const Kernel &k, int b, int row0, int pos,
                                         bool mapped, bool masked, int lane, Acc<D, NT> &acc) {
   Tile<D> t;
@@ -304,9 +336,11 @@ __device__ __forceinline__ void do_tile(uint32_t sm, const Reads<D> &at, const u
     for (int j = 0; j < 4; ++j) c0[j] = hmul2(c0[j], s0), c1[j] = hmul2(c1[j], s1);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      if (w == 0) mma16816_first(s[n], c0[0], c1[0], c0[1], c1[1], q[n][4 * w], q[n][4 * w + 1]);
-      else mma16816(s[n], c0[0], c1[0], c0[1], c1[1], q[n][4 * w], q[n][4 * w + 1]);
-      mma16816(s[n], c0[2], c1[2], c0[3], c1[3], q[n][4 * w + 2], q[n][4 * w + 3]);
+      uint32_t f[4];
+      q.get(n, w, f);
+      if (w == 0) mma16816_first(s[n], c0[0], c1[0], c0[1], c1[1], f[0], f[1]);
+      else mma16816(s[n], c0[0], c1[0], c0[1], c1[1], f[0], f[1]);
+      mma16816(s[n], c0[2], c1[2], c0[3], c1[3], f[2], f[3]);
     }
   }
   read_values<D>(sm, at, t);
@@ -484,26 +518,27 @@ __device__ __forceinline__ void store_whole(const Kernel &k, const Rows &rows, i
 // their largest element to 2^14..2^15 (2^126 at most: bf16 values are multiples of 2^-133).
 template <int D, int NT>
 __device__ __forceinline__ void load_queries(const Kernel &k, const Rows &rows, int b, int h, int row0, int lane,
-                                             uint32_t (&q)[NT][D / 8], float (&mul)[NT][2]) {
+                                             Queries<D, NT> &queries, float (&mul)[NT][2]) {
   const int g = lane >> 2, tig = lane & 3;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int row = row0 + 8 * n + g;
+    uint32_t q[D / 8];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) q[n][i] = 0u;
+    for (int i = 0; i < D / 8; ++i) q[i] = 0u;
     if (row / k.G < rows.count) {
       const uint4 *src = reinterpret_cast<const uint4 *>(k.q + out_row(k, b, h, row) * D + tig * (D / 4));
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const uint4 v = __ldg(src + i);
-        q[n][4 * i] = v.x, q[n][4 * i + 1] = v.y, q[n][4 * i + 2] = v.z, q[n][4 * i + 3] = v.w;
+        q[4 * i] = v.x, q[4 * i + 1] = v.y, q[4 * i + 2] = v.z, q[4 * i + 3] = v.w;
       }
     }
     int e = 0;
     if (k.bf16) {
       uint32_t top = 0; // the largest magnitude in each half, as bits; infinities and NaN stand above
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) top = __vmaxu2(top, q[n][i] & 0x7FFF7FFFu);
+      for (int i = 0; i < D / 8; ++i) top = __vmaxu2(top, q[i] & 0x7FFF7FFFu);
       top = max(top >> 16, top & 0xFFFFu);
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -511,8 +546,9 @@ __device__ __forceinline__ void load_queries(const Kernel &k, const Rows &rows, 
       e = top == 0 || field == 255 ? 0 : min(141 - field, 126);
       const float f = __uint_as_float((127 + e) << 23);
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) q[n][i] = pack_h2(bf16_lo(q[n][i]) * f, bf16_hi(q[n][i]) * f);
+      for (int i = 0; i < D / 8; ++i) q[i] = pack_h2(bf16_lo(q[i]) * f, bf16_hi(q[i]) * f);
     }
+    queries.put(n, q);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int ec = __shfl_sync(0xffffffffu, e, (2 * tig + c) * 4);
@@ -593,11 +629,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) mx_decode_kernel(
     const uint32_t sdst = __shfl_sync(0xffffffffu, 16 * D + (lane & (D / 8 - 1)) * 16, lane);
     uint32_t chunk = 0, schunk = 0;
     const int page_tiles = 1 << (k.c.pshift - 4);
-    const int *entry;            // table entry behind next_page's
-    int run, left_tiles;         // tiles left on the current page, and of the unit's behind it
-    int next_page;               // the page behind the current one, read ahead
+    const int *entry = nullptr;  // table entry behind next_page's
+    int run = 0, left_tiles = 0; // tiles left on the current page, and of the unit's behind it
+    int next_page = -1;          // the page behind the current one, read ahead
     uint32_t head;               // first record of the head in page 0
-    unsigned mapped = 0, ok;     // a bit for each copied tile, the latest lowest; the current page's
+    unsigned mapped = 0, ok = 0; // a bit for each copied tile, the latest lowest; the current page's
     // Unmapped pages, and what is behind the stretch's end, copy records of page 0: never looked at, and
     // cheaper than a branch for every tile.
     auto enter_page = [&](int in_page) {
@@ -621,7 +657,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) mx_decode_kernel(
       left_tiles = max(c.end(len) - tile, 0); // 0: the stretch begins with the cost of a unit
       entry = k.c.bt + static_cast<long long>(c.b) * k.c.maxp + (tile >> (k.c.pshift - 4));
       head = static_cast<uint32_t>(c.h) << k.c.pshift;
-      run = 0;
       if (left_tiles > 0) {
         next_page = __ldg(entry++);
         enter_page(tile & (page_tiles - 1));
@@ -673,7 +708,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) mx_decode_kernel(
       const int t0 = cu.first(), t1 = cu.end(len);
       if (t0 < t1) {
       const int b = cu.b, h = cu.h, row0 = cu.rb * R;
-      uint32_t q[NT][D / 8];
+      Queries<D, NT> q; // each lane reads what it wrote
+      q.bind(ring_addr + S * C::kTile + lane * 16);
       float mul[NT][2];
       int full; // every row of the block sees the positions below
       {
@@ -704,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) mx_decode_kernel(
       }
       if (t0 > 0) {
         left |= kHead | (t1 == cu.nt ? kHeadEnds : 0);
-        store_partial<D, NT>(reinterpret_cast<float *>(ring + S * C::kTile), acc, lane);
+        store_partial<D, NT>(reinterpret_cast<float *>(ring + C::kHeadAt), acc, lane);
       } else if (t1 == cu.nt) {
         store_whole<D, NT>(k, rows_of(k, b), b, h, row0, acc, lane);
       } else { // the last unit of the stretch: its partial takes the ring's place
@@ -761,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) mx_decode_kernel(
       float ref = kRefEmpty;
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        src[w] = reinterpret_cast<const float *>(sm + w * C::kWarpBytes + (w == first ? 0 : S * C::kTile));
+        src[w] = reinterpret_cast<const float *>(sm + w * C::kWarpBytes + (w == first ? 0 : C::kHeadAt));
         st[w] = parts >> w & 1u ? *reinterpret_cast<const float2 *>(src[w] + R * D + 2 * r) : make_float2(kRefEmpty, 0.0f);
         ref = fmaxf(ref, st[w].x);
       }
