@@ -16,7 +16,8 @@
 // The softmax reference of a row moves only when a score passes it by 2^15 (a vote in the warp);
 // the frequent path has no cross-lane reduction.
 //
-// Work: the space of 16-token tiles of all (sequence, KV head, row block) units is flattened and
+// A step takes 32 tokens (two such tiles): with 16 a third more instructions went to copies, waits
+// and votes. Work: the space of 32-token tiles of all (sequence, KV head, row block) units is flattened and
 // divided evenly over all warps of the grid on the device, from the lengths in device memory, so a
 // captured graph follows lengths that change and a ragged batch stays balanced. A unit counts
 // kUnitCost tiles more than it has (queries, page table, output). Each warp copies its own tiles
@@ -40,7 +41,8 @@ constexpr float kRefDrop = 11.0f;  // the reference sits 2^11 below the largest 
 constexpr float kRefSlack = 15.0f; // ... and follows when a weight would pass 2^15 (fp16 ends at 2^16)
 constexpr float kRefEmpty = -FLT_MAX;
 constexpr int kUnitCost = 2; // what a unit costs besides its tiles, in tiles
-constexpr int kMinTiles = 3; // tiles a warp gets at least (unit costs included)
+constexpr int kMinTiles = 2; // tiles a warp gets at least (unit costs included)
+constexpr int kSub = 2;      // 16-token MMA tiles of a tile
 
 // Shapes of the grid: CTAs of an SM, tiles in a warp's ring.
 constexpr int kWarps = 4;
@@ -49,8 +51,9 @@ template <int D, int NT>
 struct Cfg {
   static constexpr int kCtas = D == 64 && NT == 1 ? 4 : D == 256 || (D == 128 && NT > 1) ? 2 : 3;
   static constexpr bool kQueriesInSmem = NT > 1;       // the registers hold NT times the sums
-  static constexpr int kStages = D == 64 ? 6 : 4;
-  static constexpr int kTile = 18 * D;                 // bytes: 16 x (D/2 + D/16) of keys and of values
+  static constexpr int kStages = D == 64 ? (NT == 1 ? 4 : 3) : D == 128 && NT < 3 ? 3 : 2;
+  static constexpr int kHalf = 18 * D;                 // bytes: 16 x (D/2 + D/16) of keys and of values
+  static constexpr int kTile = kSub * kHalf;
   static constexpr int kSlot = 8 * NT * (D + 2) * 4;   // bytes of a partial: sums, then (reference, weight sum)
   static constexpr int kQueries = kQueriesInSmem ? 16 * D * NT : 0;
   static constexpr int kWarpBytes = kStages * kTile + kSlot + kQueries;
@@ -68,6 +71,7 @@ struct Kernel {
   float *part;   // [2 * ctas] partials (Cfg::kSlot)
   int4 *desc;    // [ctas]: {sequence, head, first row, number of CTAs} of the unit cut at its end
   int Hq, G, Lq, row_blocks, bf16, out_dtype;
+  float inv_group;   // 1 / G
   float scale, klog; // softmax scale; log2(e) * key scale (apart: their product may not fit where a row's does)
 };
 
@@ -89,7 +93,12 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 __device__ __forceinline__ int tiles_of(const Kernel &k, int b) {
   if (clamp_count(k.counts, b, k.Lq) == 0) return 0;
   const int cap = k.c.maxp << k.c.pshift;
-  return (min(max(__ldg(k.lens + b), 0), cap) + 15) >> 4;
+  return (min(max(__ldg(k.lens + b), 0), cap) + 31) >> 5;
+}
+// Row r of a unit is query r / G, head r % G of the group. The quotient is at most 40 and G below
+// 2^16, so the float product is off by less than the half step that separates it from a whole number.
+__device__ __forceinline__ int query_of(const Kernel &k, int row) {
+  return static_cast<int>((static_cast<float>(row) + 0.5f) * k.inv_group);
 }
 
 __device__ __forceinline__ void store_out(const Kernel &k, long long i, float a, float b) {
@@ -219,6 +228,10 @@ struct Cursor {
   }
   __device__ __forceinline__ int first() const { return max(-at, 0); }
   __device__ __forceinline__ int end(int len) const { return min(max(len - at, 0), nt); }
+  // 16-token tiles from the unit's begin to its end within the stretch
+  __device__ __forceinline__ int end16(const Kernel &k, int len) const {
+    return min(2 * end(len), (rows_of(k, b).seen + 15) >> 4);
+  }
   // the next unit that begins within the stretch; false at its end
   __device__ __forceinline__ bool next(const Kernel &k, int len) {
     at += nt + kUnitCost;
@@ -310,80 +323,59 @@ struct Queries<D, NT, true> {
   __device__ __forceinline__ void get(int n, int w, uint32_t (&x)[4]) const { lds(at + (n * (D / 32) + w) * 512, x); }
 };
 
-// One tile. masked: some row of the block does not see every token of the tile, or its page is
-// unmapped.
+// One tile of 32 tokens from position pos. mapped: bits 1 and 0 for its first and second 16 tokens;
+// masked: some row of the block does not see every token.
 template <int D, int NT>
 __device__ __forceinline__ void do_tile(uint32_t sm, const Reads<D> &at, const Queries<D, NT> &q,
                                         const float (&mul)[NT][2], const Kernel &k, int b, int row0, int pos,
-                                        bool mapped, bool masked, int lane, Acc<D, NT> &acc) {
-  Tile<D> t;
-  read_keys<D>(sm, at, t);
-  // the scales of the lane's D/64 blocks, as fp16 pairs
-  uint32_t scale2[2][(D + 64) / 128];
+                                        unsigned mapped, bool masked, int lane, Acc<D, NT> &acc) {
+  constexpr int kScales = (D + 64) / 128;
+  float s[kSub][NT][4];
+  {
+    Tile<D> t[kSub];
+    uint32_t scale2[kSub][2][kScales]; // the scales of the lane's D/64 blocks, as fp16 pairs
 #pragma unroll
-  for (int r = 0; r < 2; ++r)
+    for (int u = 0; u < kSub; ++u) {
+      read_keys<D>(sm + u * 18 * D, at, t[u]);
 #pragma unroll
-    for (int i = 0; i < (D + 64) / 128; ++i) scale2[r][i] = e4m3_to_h2(t.ks[r] >> (16 * i));
-  float s[NT][4];
+      for (int r = 0; r < 2; ++r)
 #pragma unroll
-  for (int w = 0; w < D / 32; ++w) {
-    uint32_t c0[4], c1[4];
-    e2m1_to_h2(t.k[0][w], c0);
-    e2m1_to_h2(t.k[1][w], c1);
-    const uint32_t sel = w / 2 % 2 ? 0x3232u : 0x1010u; // the scale of this word's block, in both halves
-    const uint32_t s0 = prmt(scale2[0][w / 4], 0u, sel), s1 = prmt(scale2[1][w / 4], 0u, sel);
+        for (int i = 0; i < kScales; ++i) scale2[u][r][i] = e4m3_to_h2(t[u].ks[r] >> (16 * i));
+    }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) c0[j] = hmul2(c0[j], s0), c1[j] = hmul2(c1[j], s1);
+    for (int w = 0; w < D / 32; ++w) {
+      uint32_t c[kSub][2][4];
+      const uint32_t sel = w / 2 % 2 ? 0x3232u : 0x1010u; // the scale of this word's block, in both halves
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      uint32_t f[4];
-      q.get(n, w, f);
-      if (w == 0) mma16816_first(s[n], c0[0], c1[0], c0[1], c1[1], f[0], f[1]);
-      else mma16816(s[n], c0[0], c1[0], c0[1], c1[1], f[0], f[1]);
-      mma16816(s[n], c0[2], c1[2], c0[3], c1[3], f[2], f[3]);
+      for (int u = 0; u < kSub; ++u)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          e2m1_to_h2(t[u].k[r][w], c[u][r]);
+          const uint32_t sc = prmt(scale2[u][r][w / 4], 0u, sel);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) c[u][r][j] = hmul2(c[u][r][j], sc);
+        }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        uint32_t f[4];
+        q.get(n, w, f);
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+          if (w == 0) mma16816_first(s[u][n], c[u][0][0], c[u][1][0], c[u][0][1], c[u][1][1], f[0], f[1]);
+          else mma16816(s[u][n], c[u][0][0], c[u][1][0], c[u][0][1], c[u][1][1], f[0], f[1]);
+        }
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) mma16816(s[u][n], c[u][0][2], c[u][1][2], c[u][0][3], c[u][1][3], f[2], f[3]);
+      }
     }
   }
-  read_values<D>(sm, at, t);
-  float x[NT][4]; // logits (log2 units) less the column's reference
+  float x[kSub][NT][4]; // logits (log2 units) less the column's reference; -infinity: not seen
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[n][e] = fmaf(s[n][e], mul[n][e & 1], -acc.ref[n][e & 1]);
-  uint32_t p[NT][2];
-  auto weights = [&] { // softmax weights as the value MMAs take them; x = -infinity: not seen
-    float top = -INFINITY;
+  for (int u = 0; u < kSub; ++u)
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) top = fmaxf(top, x[n][e]);
-    if (__any_sync(0xffffffffu, top > kRefSlack)) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] = x[n][e] == -INFINITY ? x[n][e] : s[n][e] * mul[n][e & 1];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float m = fmaxf(s[n][c], s[n][c + 2]);
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          const float ref = fmaxf(acc.ref[n][c], m - kRefDrop), f = softmax_exp2(acc.ref[n][c] - ref);
-          acc.ref[n][c] = ref;
-          x[n][c] = s[n][c] - ref;
-          x[n][c + 2] = s[n][c + 2] - ref;
-          acc.l[n][c] *= f;
-          acc.l[n][c + 2] *= f;
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) acc.o[n][i][c] *= f, acc.o[n][i][c + 2] *= f;
-        }
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      p[n][0] = transpose8x8(pack_h2(softmax_exp2(x[n][0]), softmax_exp2(x[n][1])));
-      p[n][1] = transpose8x8(pack_h2(softmax_exp2(x[n][2]), softmax_exp2(x[n][3])));
-      mma16816(acc.l[n], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, p[n][0], p[n][1]);
-    }
-  };
+      for (int e = 0; e < 4; ++e) x[u][n][e] = fmaf(s[u][n][e], mul[n][e & 1], -acc.ref[n][e & 1]);
   if (masked) {
     const int g = lane >> 2, tig = lane & 3;
     const Rows rows = rows_of(k, b);
@@ -391,46 +383,99 @@ __device__ __forceinline__ void do_tile(uint32_t sm, const Reads<D> &at, const Q
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int query = (row0 + 8 * n + 2 * tig + c) / k.G;
-        const int limit = !mapped ? 0 : query < rows.count ? rows.limit(query) : rows.seen;
-        if (pos + g >= limit) x[n][c] = -INFINITY;
-        if (pos + g + 8 >= limit) x[n][c + 2] = -INFINITY;
-      }
-    // 0 * NaN is NaN: a token that a row does not see must not reach it through its scale either.
-    // Tokens that no row sees get scale 0. A NaN scale among the rest of a masked tile is rare;
-    // then each query of the block takes its own pass with only its own tokens and columns.
-    bool nan = false;
+        const int query = query_of(k, row0 + 8 * n + 2 * tig + c);
+        const int limit = (query < rows.count ? rows.limit(query) : rows.seen) - pos - g;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (!mapped || pos + 2 * tig + (i >> 1) * 8 + (i & 1) >= rows.seen) t.vs[i] = 0u;
-      nan |= (t.vs[i] & 0x7Fu) == 0x7Fu || (t.vs[i] & 0x7F00u) == 0x7F00u;
-    }
-    if (__any_sync(0xffffffffu, nan)) {
-      weights();
-      const int last = min((row0 + 8 * NT - 1) / k.G, rows.count - 1);
-      for (int query = row0 / k.G; query <= last; ++query) {
-        const int lim = rows.limit(query);
-        uint32_t pq[NT][2], vq[4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const bool mine = (row0 + 8 * n + g) / k.G == query; // a fragment's column is row g
-          pq[n][0] = mine ? p[n][0] : 0u;
-          pq[n][1] = mine ? p[n][1] : 0u;
+        for (int u = 0; u < kSub; ++u) {
+          const bool here = mapped >> (kSub - 1 - u) & 1u;
+          if (!here || 16 * u >= limit) x[u][n][c] = -INFINITY;
+          if (!here || 16 * u + 8 >= limit) x[u][n][c + 2] = -INFINITY;
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) vq[i] = pos + 2 * tig + (i >> 1) * 8 + (i & 1) < lim ? t.vs[i] : 0u;
-        // columns of other queries still meet this pass's NaN scales, with weight 0
-        unsigned own = 0;
-#pragma unroll
-        for (int i = 0; i < 2 * NT; ++i)
-          own |= static_cast<unsigned>((row0 + 8 * (i >> 1) + 2 * tig + (i & 1)) / k.G == query) << i;
-        add_values<D, NT, true>(t, vq, pq, acc, own);
       }
-      return;
+  }
+  float top = -INFINITY;
+#pragma unroll
+  for (int u = 0; u < kSub; ++u)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = fmaxf(top, x[u][n][e]);
+  if (__any_sync(0xffffffffu, top > kRefSlack)) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+          for (int e = c; e < 4; e += 2) {
+            s[u][n][e] = x[u][n][e] == -INFINITY ? x[u][n][e] : s[u][n][e] * mul[n][c];
+            m = fmaxf(m, s[u][n][e]);
+          }
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float ref = fmaxf(acc.ref[n][c], m - kRefDrop), f = softmax_exp2(acc.ref[n][c] - ref);
+        acc.ref[n][c] = ref;
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) x[u][n][c] = s[u][n][c] - ref, x[u][n][c + 2] = s[u][n][c + 2] - ref;
+        acc.l[n][c] *= f;
+        acc.l[n][c + 2] *= f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) acc.o[n][i][c] *= f, acc.o[n][i][c + 2] *= f;
+      }
     }
   }
-  weights();
-  add_values<D, NT, false>(t, t.vs, p, acc);
+#pragma unroll
+  for (int u = 0; u < kSub; ++u) {
+    Tile<D> t;
+    read_values<D>(sm + u * 18 * D, at, t);
+    uint32_t p[NT][2]; // the weights as the value MMAs take them
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      p[n][0] = transpose8x8(pack_h2(softmax_exp2(x[u][n][0]), softmax_exp2(x[u][n][1])));
+      p[n][1] = transpose8x8(pack_h2(softmax_exp2(x[u][n][2]), softmax_exp2(x[u][n][3])));
+      mma16816(acc.l[n], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, p[n][0], p[n][1]);
+    }
+    if (masked) {
+      // 0 * NaN is NaN: a token that a row does not see must not reach it through its scale either.
+      // Tokens that no row sees get scale 0. A NaN scale among the rest of a masked tile is rare;
+      // then each query of the block takes its own pass with only its own tokens and columns.
+      const int g = lane >> 2, tig = lane & 3;
+      const Rows rows = rows_of(k, b);
+      const int token = pos + 16 * u + 2 * tig;
+      const bool here = mapped >> (kSub - 1 - u) & 1u;
+      bool nan = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (!here || token + (i >> 1) * 8 + (i & 1) >= rows.seen) t.vs[i] = 0u;
+        nan |= (t.vs[i] & 0x7Fu) == 0x7Fu || (t.vs[i] & 0x7F00u) == 0x7F00u;
+      }
+      if (__any_sync(0xffffffffu, nan)) {
+        const int last = min(query_of(k, row0 + 8 * NT - 1), rows.count - 1);
+        for (int query = query_of(k, row0); query <= last; ++query) {
+          const int lim = rows.limit(query);
+          uint32_t pq[NT][2], vq[4];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const bool mine = query_of(k, row0 + 8 * n + g) == query; // a fragment's column is row g
+            pq[n][0] = mine ? p[n][0] : 0u;
+            pq[n][1] = mine ? p[n][1] : 0u;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vq[i] = token + (i >> 1) * 8 + (i & 1) < lim ? t.vs[i] : 0u;
+          // columns of other queries still meet this pass's NaN scales, with weight 0
+          unsigned own = 0;
+#pragma unroll
+          for (int i = 0; i < 2 * NT; ++i)
+            own |= static_cast<unsigned>(query_of(k, row0 + 8 * (i >> 1) + 2 * tig + (i & 1)) == query) << i;
+          add_values<D, NT, true>(t, vq, pq, acc, own);
+        }
+        continue;
+      }
+    }
+    add_values<D, NT, false>(t, t.vs, p, acc);
+  }
 }
 
 constexpr int kCombineThreads = 256;
@@ -475,7 +520,8 @@ __device__ __forceinline__ void store_partial(float *slot, const Acc<D, NT> &acc
 }
 
 __device__ __forceinline__ long long out_row(const Kernel &k, int b, int h, int row) {
-  return (static_cast<long long>(b) * k.Lq + row / k.G) * k.Hq + h * k.G + row % k.G;
+  const int query = query_of(k, row);
+  return (static_cast<long long>(b) * k.Lq + query) * k.Hq + h * k.G + row - query * k.G;
 }
 
 // Writes four elements of an output row from its sums. The largest weight is 2^11 or more: a sum of 0
@@ -483,8 +529,8 @@ __device__ __forceinline__ long long out_row(const Kernel &k, int b, int h, int 
 template <int D>
 __device__ __forceinline__ void store_row(const Kernel &k, const Rows &rows, int b, int h, int row, int d, float l,
                                           const float4 &o) {
-  const bool some = rows.limit(row / k.G) > 0 && l != 0.0f;
-  const float inv = k.c.g[1] / l;
+  const bool some = rows.limit(query_of(k, row)) > 0 && l != 0.0f;
+  const float inv = __fdividef(k.c.g[1], l); // off by 2 units in the last place
   const long long at = out_row(k, b, h, row) * D + d;
   store_out(k, at, some ? o.x * inv : 0.0f, some ? o.y * inv : 0.0f);
   store_out(k, at + 2, some ? o.z * inv : 0.0f, some ? o.w * inv : 0.0f);
@@ -501,15 +547,28 @@ __device__ __forceinline__ void store_whole(const Kernel &k, const Rows &rows, i
     for (int c = 0; c < 2; ++c) {
       const int row = row0 + 8 * n + 2 * tig + c;
       if (row >= k.Lq * k.G) continue;
-      const bool some = rows.limit(row / k.G) > 0 && acc.l[n][c] != 0.0f; // as in store_row
-      const float inv = k.c.g[1] / acc.l[n][c];
+      const bool some = rows.limit(query_of(k, row)) > 0 && acc.l[n][c] != 0.0f; // as in store_row
+      const float inv = some ? __fdividef(k.c.g[1], acc.l[n][c]) : 0.0f;
+      const size_t at = static_cast<size_t>(out_row(k, b, h, row) * D + g * (D / 8));
       float x[D / 8];
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         x[2 * i] = some ? acc.o[n][i][c] * inv : 0.0f;
         x[2 * i + 1] = some ? acc.o[n][i][c + 2] * inv : 0.0f;
       }
-      store_vec<D / 8>(k.out, k.out_dtype, static_cast<size_t>(out_row(k, b, h, row) * D + g * (D / 8)), x);
+      if (k.out_dtype == TQ_F32) {
+        store_vec<D / 8>(k.out, TQ_F32, at, x);
+      } else {
+        uint32_t w[D / 16];
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+          w[i] = k.out_dtype == TQ_BF16 ? *reinterpret_cast<const uint32_t *>(&v) : pack_h2(x[2 * i], x[2 * i + 1]);
+        }
+        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(k.out) + at);
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+      }
     }
 }
 
@@ -526,7 +585,7 @@ __device__ __forceinline__ void load_queries(const Kernel &k, const Rows &rows, 
     uint32_t q[D / 8];
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) q[i] = 0u;
-    if (row / k.G < rows.count) {
+    if (query_of(k, row) < rows.count) {
       const uint4 *src = reinterpret_cast<const uint4 *>(k.q + out_row(k, b, h, row) * D + tig * (D / 4));
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
@@ -621,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) mx_decode_kernel(
   int left = 0;
   if (len > 0) {
     const uint32_t ring_addr = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
-    // ---- copies run S - 1 tiles ahead; `run` tiles, from record rec, are left on the current page
+    // ---- copies run S - 1 tiles ahead
     // the lane's 16 bytes of the next tile: `chunk` in the codes, `schunk` in the scales (keys' in the first
     // half of D/8 lanes, values' in the second; further lanes repeat them)
     const uint8_t *sc = k.c.scales[lane / (D / 16) & 1];
@@ -630,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) mx_decode_kernel(
     uint32_t chunk = 0, schunk = 0;
     const int page_tiles = 1 << (k.c.pshift - 4);
     const int *entry = nullptr;  // table entry behind next_page's
-    int run = 0, left_tiles = 0; // tiles left on the current page, and of the unit's behind it
+    int run = 0, left_tiles = 0; // 16-token tiles left on the current page, and of the unit's behind it
     int next_page = -1;          // the page behind the current one, read ahead
     uint32_t head;               // first record of the head in page 0
     unsigned mapped = 0, ok = 0; // a bit for each copied tile, the latest lowest; the current page's
@@ -653,8 +712,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) mx_decode_kernel(
       Cursor c;
       c.start(k, s_b0[warp], s_ahead[warp]);
       s_done[warp] = s_copy[warp] = c;
-      const int tile = c.first();
-      left_tiles = max(c.end(len) - tile, 0); // 0: the stretch begins with the cost of a unit
+      const int tile = kSub * c.first();
+      left_tiles = max(c.end16(k, len) - tile, 0); // 0: the stretch begins with the cost of a unit
       entry = k.c.bt + static_cast<long long>(c.b) * k.c.maxp + (tile >> (k.c.pshift - 4));
       head = static_cast<uint32_t>(c.h) << k.c.pshift;
       if (left_tiles > 0) {
@@ -663,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) mx_decode_kernel(
       }
     }
     __syncwarp();
-    auto copy_tile = [&](uint32_t dst) {
+    auto copy_half = [&](uint32_t dst) {
       if (run == 0) {
         if (left_tiles == 0) { // the next unit with tiles in the stretch
           Cursor c = s_copy[warp];
@@ -672,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) mx_decode_kernel(
           while (more && c.end(len) == 0);
           next_page = -1;
           if (more) {
-            left_tiles = c.end(len);
+            left_tiles = c.end16(k, len);
             entry = k.c.bt + static_cast<long long>(c.b) * k.c.maxp;
             head = static_cast<uint32_t>(c.h) << k.c.pshift;
             next_page = __ldg(entry++);
@@ -691,11 +750,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) mx_decode_kernel(
         copy16(to + 8 * D, b + j * 512);
       }
       copy16(dst + sdst, sc + static_cast<size_t>(schunk) * 16);
-      asm volatile("cp.async.commit_group;" ::: "memory");
       chunk += D / 2;
       schunk += D / 16;
       --run;
       mapped = 2 * mapped + ok;
+    };
+    auto copy_tile = [&](uint32_t dst) {
+      copy_half(dst);
+      if (run | left_tiles) copy_half(dst + C::kHalf);
+      else mapped *= 2; // the unit ends with the first half
+      asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) copy_tile(ring_addr + i * C::kTile);
@@ -715,7 +779,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) mx_decode_kernel(
       {
         const Rows rows = rows_of(k, b);
         load_queries<D, NT>(k, rows, b, h, row0, lane, q, mul);
-        full = row0 / k.G < rows.count ? rows.limit(row0 / k.G) : rows.seen;
+        const int query = query_of(k, row0);
+        full = query < rows.count ? rows.limit(query) : rows.seen;
       }
       Acc<D, NT> acc;
 #pragma unroll
@@ -732,9 +797,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) mx_decode_kernel(
         asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
         __syncwarp(); // all lanes' copies of this tile are there, and the oldest stage's readers are done
         copy_tile(ring_addr + free_stage);
-        const bool here = mapped >> (S - 1) & 1u;
-        const int pos = tile << 4;
-        do_tile<D, NT>(ring_addr + at_stage, reads, q, mul, k, b, row0, pos, here, pos + 16 > full || !here, lane, acc);
+        const unsigned here = mapped >> (2 * (S - 1)) & 3u;
+        const int pos = tile << 5;
+        do_tile<D, NT>(ring_addr + at_stage, reads, q, mul, k, b, row0, pos, here, pos + 32 > full || here != 3u, lane, acc);
         free_stage = at_stage;
         at_stage = at_stage + C::kTile == S * C::kTile ? 0 : at_stage + C::kTile;
       }
@@ -915,6 +980,7 @@ cudaError_t launch_mx_decode(const MxDecodeArgs &a, cudaStream_t s) {
   k.part = reinterpret_cast<float *>(k.desc + a.plan.ctas);
   k.Hq = a.Hq;
   k.G = a.Hq / a.c.Hkv;
+  k.inv_group = 1.0f / static_cast<float>(k.G);
   k.Lq = a.Lq;
   k.row_blocks = a.plan.row_blocks;
   k.bf16 = a.dtype == TQ_BF16;
