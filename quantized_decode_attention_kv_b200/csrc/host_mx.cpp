@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <exception>
@@ -22,11 +23,15 @@ int cuda_status(cudaError_t e, const char *what) {
   return e == cudaSuccess ? TQ_OK : fail(TQ_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-int sm_count(int *n) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+// The current device and its SM count, asked for once per device.
+int current_device(int *dev, int *sms) {
+  static std::atomic<int> known[64];
+  if (cudaGetDevice(dev) != cudaSuccess) return fail(TQ_ERR_CUDA, "cannot query the current device");
+  *sms = *dev < 64 ? known[*dev].load(std::memory_order_relaxed) : 0;
+  if (*sms) return TQ_OK;
+  if (cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev) != cudaSuccess)
     return fail(TQ_ERR_CUDA, "cannot query the device's SM count");
+  if (*dev < 64) known[*dev].store(*sms, std::memory_order_relaxed);
   return TQ_OK;
 }
 
@@ -114,12 +119,12 @@ int check_decode_shape(int Hq, int Lq, const tq_mx_cache *cache, tq::MxDecodeArg
   if (cache->B * blocks * cache->Hkv * tiles >= 4294967296.0)
     return fail(TQ_ERR_INVALID_ARG, "B=%d x Hkv=%d x %d positions are too many for one call", cache->B, cache->Hkv,
                 cache->max_pages * cache->page_size);
-  int sms = 0;
-  st = sm_count(&sms);
+  int dev = 0, sms = 0;
+  st = current_device(&dev, &sms);
   if (st) return st;
   a->Hq = Hq;
   a->Lq = Lq;
-  a->plan = tq::plan_mx_decode(cache->Hkv, cache->d, Hq, Lq, sms);
+  a->plan = tq::plan_mx_decode(cache->Hkv, cache->d, Hq, Lq, dev, sms);
   return TQ_OK;
 }
 
@@ -276,8 +281,8 @@ int tq_pages_fork(const tq_page_pool *pool, const tq_page_array *arrays, int n_a
     return fail(TQ_ERR_INVALID_ARG, "parent_of/status must be non-NULL and 4-byte aligned");
   st = check_workspace(ws, ws_bytes, tq::pages_workspace_bytes(*pool));
   if (st) return st;
-  int sms = 0;
-  st = sm_count(&sms);
+  int dev = 0, sms = 0;
+  st = current_device(&dev, &sms);
   if (st) return st;
   return cuda_status(tq::launch_pages_fork(*pool, arrays, n_arrays, parent_of, status, ws, sms,
                                            static_cast<cudaStream_t>(stream)), "page fork launch");
@@ -299,8 +304,8 @@ int tq_pages_compact(const tq_page_pool *pool, const tq_page_array *arrays, int 
   if (!aligned(live, 4)) return fail(TQ_ERR_INVALID_ARG, "live must be non-NULL and 4-byte aligned");
   st = check_workspace(ws, ws_bytes, tq::pages_workspace_bytes(*pool));
   if (st) return st;
-  int sms = 0;
-  st = sm_count(&sms);
+  int dev = 0, sms = 0;
+  st = current_device(&dev, &sms);
   if (st) return st;
   return cuda_status(tq::launch_pages_compact(*pool, arrays, n_arrays, live, ws, sms,
                                               static_cast<cudaStream_t>(stream)), "page compact launch");
@@ -327,8 +332,8 @@ int tq_pages_copy(const tq_page_array *arrays, int n_arrays, int num_pages, cons
   } catch (const std::exception &) {
     return fail(TQ_ERR_INVALID_ARG, "out of host memory for %d pairs", n);
   }
-  int sms = 0;
-  st = sm_count(&sms);
+  int dev = 0, sms = 0;
+  st = current_device(&dev, &sms);
   if (st) return st;
   return cuda_status(tq::launch_pages_copy(arrays, n_arrays, src, dst, n, sms, static_cast<cudaStream_t>(stream)),
                      "page copy launch");

@@ -26,7 +26,9 @@
 // shared memory, joined by the CTA, and those cut by a CTA boundary in the workspace, joined by the
 // combine kernel.
 #include <algorithm>
+#include <atomic>
 #include <cfloat>
+#include <type_traits>
 
 #include "mma_ops.cuh"
 #include "mx.cuh"
@@ -49,11 +51,11 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 template <int D, int NT>
 struct Cfg {
-  static constexpr int kCtas = D == 64 && NT == 1 ? 4 : D == 256 || (D == 128 && NT > 1) ? 2 : 3;
+  static constexpr int kCtas = D == 64 && NT == 1 ? 4 : D == 256 || NT == 3 || (D == 128 && NT == 2) ? 2 : 3;
   static constexpr bool kQueriesInSmem = NT > 1;       // the registers hold NT times the sums
-  static constexpr int kStages = D == 64 ? (NT == 1 ? 4 : 3) : D == 128 && NT < 3 ? 3 : 2;
-  static constexpr int kHalf = 18 * D;                 // bytes: 16 x (D/2 + D/16) of keys and of values
-  static constexpr int kTile = kSub * kHalf;
+  static constexpr int kStages = D == 64 || (D == 128 && NT < 3) ? 3 : 2;
+  static constexpr int kSixteen = 18 * D;                 // bytes: 16 x (D/2 + D/16) of keys and of values
+  static constexpr int kTile = kSub * kSixteen;
   static constexpr int kSlot = 8 * NT * (D + 2) * 4;   // bytes of a partial: sums, then (reference, weight sum)
   static constexpr int kQueries = kQueriesInSmem ? 16 * D * NT : 0;
   static constexpr int kWarpBytes = kStages * kTile + kSlot + kQueries;
@@ -93,7 +95,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 __device__ __forceinline__ int tiles_of(const Kernel &k, int b) {
   if (clamp_count(k.counts, b, k.Lq) == 0) return 0;
   const int cap = k.c.maxp << k.c.pshift;
-  return (min(max(__ldg(k.lens + b), 0), cap) + 31) >> 5;
+  return (min(max(__ldg(k.lens + b), 0), cap) + 16 * kSub - 1) / (16 * kSub);
 }
 // Row r of a unit is query r / G, head r % G of the group. The quotient is at most 40 and G below
 // 2^16, so the float product is off by less than the half step that separates it from a whole number.
@@ -230,7 +232,7 @@ struct Cursor {
   __device__ __forceinline__ int end(int len) const { return min(max(len - at, 0), nt); }
   // 16-token tiles from the unit's begin to its end within the stretch
   __device__ __forceinline__ int end16(const Kernel &k, int len) const {
-    return min(2 * end(len), (rows_of(k, b).seen + 15) >> 4);
+    return min(kSub * end(len), (rows_of(k, b).seen + 15) >> 4);
   }
   // the next unit that begins within the stretch; false at its end
   __device__ __forceinline__ bool next(const Kernel &k, int len) {
@@ -323,8 +325,7 @@ struct Queries<D, NT, true> {
   __device__ __forceinline__ void get(int n, int w, uint32_t (&x)[4]) const { lds(at + (n * (D / 32) + w) * 512, x); }
 };
 
-// One tile of 32 tokens from position pos. mapped: bits 1 and 0 for its first and second 16 tokens;
-// masked: some row of the block does not see every token.
+// One tile from position pos. mapped: a bit for each 16 tokens, the first highest; masked: some row of the block does not see every token.
 template <int D, int NT>
 __device__ __forceinline__ void do_tile(uint32_t sm, const Reads<D> &at, const Queries<D, NT> &q,
                                         const float (&mul)[NT][2], const Kernel &k, int b, int row0, int pos,
@@ -692,11 +693,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) mx_decode_kernel(
     int run = 0, left_tiles = 0; // 16-token tiles left on the current page, and of the unit's behind it
     int next_page = -1;          // the page behind the current one, read ahead
     uint32_t head;               // first record of the head in page 0
-    unsigned mapped = 0, ok = 0; // a bit for each copied tile, the latest lowest; the current page's
+    unsigned mapped = 0, ok = 0; // a bit for each 16 tokens copied, the latest lowest; all or none for the current page
     // Unmapped pages, and what is behind the stretch's end, copy records of page 0: never looked at, and
     // cheaper than a branch for every tile.
     auto enter_page = [&](int in_page) {
-      ok = static_cast<unsigned>(next_page) < static_cast<unsigned>(k.c.num_pages);
+      ok = static_cast<unsigned>(next_page) < static_cast<unsigned>(k.c.num_pages) ? (1u << kSub) - 1u : 0u;
       // 16-byte chunks of codes < 2^32 (the host checks), so their index is one 32-bit word
       const uint32_t rec = ok ? ((next_page * static_cast<uint32_t>(k.c.Hkv)) << k.c.pshift) + head + (in_page << 4) : 0u;
       chunk = rec * (D / 32) + lane;
@@ -722,7 +723,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) mx_decode_kernel(
       }
     }
     __syncwarp();
-    auto copy_half = [&](uint32_t dst) {
+    auto copy = [&](uint32_t dst, auto subs) { // subs x 16 adjacent tokens
+      const uint8_t *a = k.c.codes[0] + static_cast<size_t>(chunk) * 16, *b = k.c.codes[1] + static_cast<size_t>(chunk) * 16;
+      const uint8_t *s = sc + static_cast<size_t>(schunk) * 16;
+#pragma unroll
+      for (int u = 0; u < subs.value; ++u) {
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) { // 512 bytes: the swizzle of lines 4 apart differs for D = 256 only
+          const uint32_t to = dst + u * C::kSixteen + (D == 256 ? swz ^ ((j & 1) << 6) : swz) + j * 512;
+          copy16(to, a + u * 8 * D + j * 512);
+          copy16(to + 8 * D, b + u * 8 * D + j * 512);
+        }
+        copy16(dst + u * C::kSixteen + sdst, s + u * D);
+      }
+      chunk += subs.value * (D / 2);
+      schunk += subs.value * (D / 16);
+    };
+    auto copy16_tokens = [&](uint32_t dst) {
       if (run == 0) {
         if (left_tiles == 0) { // the next unit with tiles in the stretch
           Cursor c = s_copy[warp];
@@ -742,23 +759,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) mx_decode_kernel(
         }
         enter_page(0);
       }
-      const uint8_t *a = k.c.codes[0] + static_cast<size_t>(chunk) * 16, *b = k.c.codes[1] + static_cast<size_t>(chunk) * 16;
-#pragma unroll
-      for (int j = 0; j < D / 64; ++j) { // 512 bytes: the swizzle of lines 4 apart differs for D = 256 only
-        const uint32_t to = dst + (D == 256 ? swz ^ ((j & 1) << 6) : swz) + j * 512;
-        copy16(to, a + j * 512);
-        copy16(to + 8 * D, b + j * 512);
-      }
-      copy16(dst + sdst, sc + static_cast<size_t>(schunk) * 16);
-      chunk += D / 2;
-      schunk += D / 16;
+      copy(dst, std::integral_constant<int, 1>{});
       --run;
-      mapped = 2 * mapped + ok;
+      mapped = 2 * mapped + (ok & 1u);
     };
     auto copy_tile = [&](uint32_t dst) {
-      copy_half(dst);
-      if (run | left_tiles) copy_half(dst + C::kHalf);
-      else mapped *= 2; // the unit ends with the first half
+      if (run >= kSub) { // within a page
+        copy(dst, std::integral_constant<int, kSub>{});
+        run -= kSub;
+        mapped = (mapped << kSub) | ok;
+      } else {
+        copy16_tokens(dst);
+#pragma unroll 1
+        for (int u = 1; u < kSub; ++u) {
+          if (run | left_tiles) copy16_tokens(dst + u * C::kSixteen);
+          else mapped *= 2; // the unit has ended
+        }
+      }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
@@ -797,9 +814,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) mx_decode_kernel(
         asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
         __syncwarp(); // all lanes' copies of this tile are there, and the oldest stage's readers are done
         copy_tile(ring_addr + free_stage);
-        const unsigned here = mapped >> (2 * (S - 1)) & 3u;
-        const int pos = tile << 5;
-        do_tile<D, NT>(ring_addr + at_stage, reads, q, mul, k, b, row0, pos, here, pos + 32 > full || here != 3u, lane, acc);
+        constexpr int kTokens = 16 * kSub;
+        constexpr unsigned kAll = (1u << kSub) - 1u;
+        const unsigned here = mapped >> (kSub * (S - 1)) & kAll;
+        const int pos = tile * kTokens;
+        do_tile<D, NT>(ring_addr + at_stage, reads, q, mul, k, b, row0, pos, here, pos + kTokens > full || here != kAll, lane, acc);
         free_stage = at_stage;
         at_stage = at_stage + C::kTile == S * C::kTile ? 0 : at_stage + C::kTile;
       }
@@ -926,8 +945,14 @@ __global__ void __launch_bounds__(kCombineThreads) mx_combine_kernel(const Kerne
 template <int D, int NT>
 cudaError_t run(const Kernel &k, const MxPlan &p, cudaStream_t s) {
   constexpr int smem = Cfg<D, NT>::kSmem;
-  cudaError_t e = cudaFuncSetAttribute(mx_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  static std::atomic<uint64_t> set{0}; // devices (the first 64) whose kernel has its shared memory size
+  const uint64_t bit = p.device < 64 ? 1ull << p.device : 0;
+  cudaError_t e = cudaSuccess;
+  if (!(set.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(mx_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    set.fetch_or(bit, std::memory_order_release);
+  }
   e = launch_pdl(mx_decode_kernel<D, NT>, dim3(p.ctas), dim3(kThreads), smem, s, k);
   if (e != cudaSuccess) return e;
   return launch_pdl(mx_combine_kernel<D, NT>, dim3(p.ctas), dim3(kCombineThreads), 0, s, k);
@@ -954,8 +979,9 @@ struct Launch {
 
 } // namespace
 
-MxPlan plan_mx_decode(int Hkv, int d, int Hq, int Lq, int sm_count) {
+MxPlan plan_mx_decode(int Hkv, int d, int Hq, int Lq, int device, int sm_count) {
   MxPlan p;
+  p.device = device;
   const int rows = Lq * (Hq / Hkv), most = d == 256 ? 1 : 3;
   p.row_blocks = (rows + 8 * most - 1) / (8 * most);
   p.nt = (rows + 8 * p.row_blocks - 1) / (8 * p.row_blocks);

@@ -206,7 +206,7 @@ cudaError_t launch_mx_read(const MxRowsArgs &a, cudaStream_t s);
 struct MxPlan {
   int nt;         // tiles of 8 query rows (query, head of the group) that a CTA holds
   int row_blocks; // blocks of 8 nt rows per (sequence, KV head)
-  int ctas;
+  int ctas, device;
   size_t ws_bytes;
 };
 struct MxDecodeArgs {
@@ -219,7 +219,7 @@ struct MxDecodeArgs {
   void *ws;
   MxPlan plan;
 };
-MxPlan plan_mx_decode(int Hkv, int d, int Hq, int Lq, int sm_count);
+MxPlan plan_mx_decode(int Hkv, int d, int Hq, int Lq, int device, int sm_count);
 cudaError_t launch_mx_decode(const MxDecodeArgs &a, cudaStream_t s);
 
 // ---------------------------------------------------------------- pages of paged caches

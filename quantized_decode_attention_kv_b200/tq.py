@@ -512,7 +512,8 @@ class TQMXCache:
         self.struct = tq_mx_cache(B, Hkv, d, page_size, num_pages, max_pages, k_scale, v_scale,
                                   t["k_codes"].data_ptr(), t["v_codes"].data_ptr(), t["k_scales"].data_ptr(),
                                   t["v_scales"].data_ptr(), block_table.data_ptr())
-        if int(lib.tq_mx_cache_arrays(ctypes.byref(self.struct), (tq_page_array * 8)())) == 0:
+        self.ref = ctypes.byref(self.struct)
+        if int(lib.tq_mx_cache_arrays(self.ref, (tq_page_array * 8)())) == 0:
             raise TQError(TQ_ERR_INVALID_ARG, last_error())
 
     def __getitem__(self, key):
@@ -522,52 +523,71 @@ class TQMXCache:
 def _run(fn, device: torch.device, stream, *args) -> None:
     """Call a libtq entry point with ``device`` current, on ``stream`` (default: the device's
     current stream)."""
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)))
+    index = device.index
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(index)  # a decode step cannot afford building a Stream
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, _stream(stream)))
+        stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if index == torch.cuda.current_device():
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, stream)
+    if status != TQ_OK:
+        raise TQError(status, last_error())
 
 
 def _i32(t, n: int, name: str, device: torch.device) -> int:
     """Pointer of a contiguous int32 tensor of n elements on the device (n < 0: at least one)."""
-    if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device or not t.is_contiguous()
-            or (t.dim() != 1 or t.shape[0] != n if n >= 0 else t.numel() < 1)):
+    if (not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.device != device or not t.is_contiguous()
+            or (t.dim() != 1 or t.numel() != n if n >= 0 else t.numel() < 1)):
         raise TQError(TQ_ERR_INVALID_ARG, f"{name} must be a contiguous int32 tensor"
                       f"{f' [{n}]' if n >= 0 else ''} on {device}")
     return t.data_ptr()
 
 
-def _mx_rows(x, cache: TQMXCache, name: str, contiguous: bool):
-    """Checks one [B, Hkv, T, d] tensor; its (pointer, strides in elements)."""
+def _ws(ws, device: torch.device) -> int:
+    if not isinstance(ws, torch.Tensor) or ws.device != device or not ws.is_contiguous():
+        raise TQError(TQ_ERR_INVALID_ARG, f"ws must be a contiguous tensor on {device}")
+    return ws.data_ptr()
+
+
+def _mx_rows(x, cache: TQMXCache, name: str):
+    """Checks one [B, Hkv, T, d] tensor; its (dtype, T)."""
+    if isinstance(x, torch.Tensor) and x.device == cache.device and x.dim() == 4:
+        B, Hkv, T, d = x.shape
+        if B == cache.B and Hkv == cache.Hkv and d == cache.d and x.dtype in _DTYPES:
+            return x.dtype, T
+        if x.dtype not in _DTYPES:
+            raise TQError(TQ_ERR_INVALID_ARG, f"{name}: unsupported dtype {x.dtype}")
+    raise TQError(TQ_ERR_INVALID_ARG, f"{name} must be a tensor [B={cache.B}][Hkv={cache.Hkv}][T][d={cache.d}] "
+                  f"on {cache.device}")
+
+
+def _mx_pair(K, V, cache: TQMXCache):
+    """(dtype, T) of K and V, either of which may be None."""
+    if K is None and V is None:
+        raise TQError(TQ_ERR_INVALID_ARG, "K and V are both None")
+    k = v = None
+    if K is not None:
+        k = v = _mx_rows(K, cache, "K")
+    if V is not None:
+        v = _mx_rows(V, cache, "V")
+    if k is not None and k != v:
+        raise TQError(TQ_ERR_INVALID_ARG, "K and V must share their dtype and T")
+    return v
+
+
+def _mx_strides(x, name: str):
+    """Pointer and row strides (in elements; None where they are those of a contiguous tensor)."""
     if x is None:
         return None, None
-    if (not isinstance(x, torch.Tensor) or x.device != cache.device or x.dim() != 4 or x.shape[0] != cache.B
-            or x.shape[1] != cache.Hkv or x.shape[3] != cache.d):
-        raise TQError(TQ_ERR_INVALID_ARG, f"{name} must be a tensor [B={cache.B}][Hkv={cache.Hkv}][T][d={cache.d}] "
-                      f"on {cache.device}")
-    if contiguous:
-        if not x.is_contiguous():
-            raise TQError(TQ_ERR_INVALID_ARG, f"{name} must be contiguous")
+    if x.is_contiguous():
         return x.data_ptr(), None
     s = x.stride()
     if s[3] != 1:
         raise TQError(TQ_ERR_INVALID_ARG, f"{name}: the elements of a row must be adjacent")
-    return x.data_ptr(), (ctypes.c_int64 * 3)(s[0], s[1], s[2])
-
-
-def _mx_pair(K, V, cache: TQMXCache, contiguous: bool):
-    ref = K if K is not None else V
-    if ref is None:
-        raise TQError(TQ_ERR_INVALID_ARG, "K and V are both None")
-    kp, ks = _mx_rows(K, cache, "K", contiguous)
-    vp, vs = _mx_rows(V, cache, "V", contiguous)
-    if K is not None and V is not None and (K.dtype != V.dtype or K.shape[2] != V.shape[2]):
-        raise TQError(TQ_ERR_INVALID_ARG, "K and V must share their dtype and T")
-    dt = _DTYPES.get(ref.dtype)
-    if dt is None:
-        raise TQError(TQ_ERR_INVALID_ARG, f"unsupported dtype {ref.dtype}")
-    return kp, ks, vp, vs, dt, ref.shape[2]
+    return x.data_ptr(), (ctypes.c_int64 * 3)(*s[:3])
 
 
 def tq_quantize_kv_mx(K: torch.Tensor | None, V: torch.Tensor | None, cache: TQMXCache, lens: torch.Tensor,
@@ -575,27 +595,30 @@ def tq_quantize_kv_mx(K: torch.Tensor | None, V: torch.Tensor | None, cache: TQM
     """Write rows of K, V [B, Hkv, T, d] (any strides whose rows are adjacent and 16-byte aligned): row
     t < counts[b] (default: T) is position lens[b] - counts[b] + t of sequence b; lens holds the
     lengths after the write. lens, counts: int32 [B] on the device."""
-    kp, ks, vp, vs, dt, T = _mx_pair(K, V, cache, False)
+    dtype, T = _mx_pair(K, V, cache)
+    kp, ks = _mx_strides(K, "K")
+    vp, vs = _mx_strides(V, "V")
     dev = cache.device
-    _run(lib.tq_quantize_kv_mx, dev, stream, kp, vp, dt, T, ks, vs, _i32(lens, cache.B, "lens", dev),
-         None if counts is None else _i32(counts, cache.B, "counts", dev), ctypes.byref(cache.struct))
+    _run(lib.tq_quantize_kv_mx, dev, stream, kp, vp, _DTYPES[dtype], T, ks, vs, _i32(lens, cache.B, "lens", dev),
+         None if counts is None else _i32(counts, cache.B, "counts", dev), cache.ref)
 
 
 def tq_dequantize_mx(cache: TQMXCache, lens: torch.Tensor, K: torch.Tensor | None, V: torch.Tensor | None,
                      counts: torch.Tensor | None = None, stream=None) -> None:
     """Read the same rows back into K, V (contiguous [B, Hkv, T, d]); rows that hold none are zeros."""
-    kp, _, vp, _, dt, T = _mx_pair(K, V, cache, True)
+    dtype, T = _mx_pair(K, V, cache)
     dev = cache.device
-    _run(lib.tq_dequantize_mx, dev, stream, ctypes.byref(cache.struct), T, _i32(lens, cache.B, "lens", dev),
-         None if counts is None else _i32(counts, cache.B, "counts", dev), kp, vp, dt)
+    for x in (K, V):
+        if x is not None and not x.is_contiguous():
+            raise TQError(TQ_ERR_INVALID_ARG, "K and V must be contiguous")
+    _run(lib.tq_dequantize_mx, dev, stream, cache.ref, T, _i32(lens, cache.B, "lens", dev),
+         None if counts is None else _i32(counts, cache.B, "counts", dev), None if K is None else K.data_ptr(),
+         None if V is None else V.data_ptr(), _DTYPES[dtype])
 
 
 def tq_decode_mx_workspace_bytes(cache: TQMXCache, Hq: int, Lq: int = 1) -> int:
-    if cache.device.index == torch.cuda.current_device():
-        n = int(lib.tq_decode_mx_workspace_bytes(Hq, Lq, ctypes.byref(cache.struct)))
-    else:
-        with torch.cuda.device(cache.device):
-            n = int(lib.tq_decode_mx_workspace_bytes(Hq, Lq, ctypes.byref(cache.struct)))
+    with torch.cuda.device(cache.device):
+        n = int(lib.tq_decode_mx_workspace_bytes(Hq, Lq, cache.ref))
     if n == 0:
         raise TQError(TQ_ERR_INVALID_ARG, last_error())
     return n
@@ -607,19 +630,20 @@ def tq_decode_attention_mx(q: torch.Tensor, cache: TQMXCache, lens: torch.Tensor
     (default: Lq) stands at position lens[b] - counts[b] + i and sees the positions up to its own;
     out [B, Lq, Hq, d] (any dtype). Queries that see nothing give zeros."""
     dev = cache.device
-    if (not isinstance(q, torch.Tensor) or q.dim() != 4 or q.shape[0] != cache.B or q.shape[3] != cache.d
-            or q.device != dev or not q.is_contiguous()):
+    if not isinstance(q, torch.Tensor) or q.dim() != 4 or q.device != dev or not q.is_contiguous():
         raise TQError(TQ_ERR_INVALID_ARG, f"q must be a contiguous tensor [B={cache.B}][Lq][Hq][d={cache.d}] on {dev}")
-    if not isinstance(out, torch.Tensor) or out.shape != q.shape or out.device != dev or not out.is_contiguous():
+    shape = q.shape
+    B, Lq, Hq, d = shape
+    if B != cache.B or d != cache.d:
+        raise TQError(TQ_ERR_INVALID_ARG, f"q must be a contiguous tensor [B={cache.B}][Lq][Hq][d={cache.d}] on {dev}")
+    if not isinstance(out, torch.Tensor) or out.shape != shape or out.device != dev or not out.is_contiguous():
         raise TQError(TQ_ERR_INVALID_ARG, f"out must be a contiguous tensor of q's shape on {dev}")
     dt, odt = _DTYPES.get(q.dtype), _DTYPES.get(out.dtype)
     if dt is None or odt is None:
         raise TQError(TQ_ERR_INVALID_ARG, f"unsupported dtypes {q.dtype}, {out.dtype}")
-    if ws.device != dev:
-        raise TQError(TQ_ERR_INVALID_ARG, f"ws must be on {dev}")
-    _run(lib.tq_decode_attention_mx, dev, stream, q.data_ptr(), dt, q.shape[2], q.shape[1],
-         _i32(lens, cache.B, "lens", dev), None if counts is None else _i32(counts, cache.B, "counts", dev), scale,
-         ctypes.byref(cache.struct), out.data_ptr(), odt, _dev(ws, "ws"), ws.numel() * ws.element_size())
+    _run(lib.tq_decode_attention_mx, dev, stream, q.data_ptr(), dt, Hq, Lq, _i32(lens, B, "lens", dev),
+         None if counts is None else _i32(counts, B, "counts", dev), scale, cache.ref, out.data_ptr(), odt,
+         _ws(ws, dev), ws.nbytes)
 
 
 # ------------------------------------------------------------------ pages of paged caches
@@ -637,6 +661,7 @@ class TQPagePool:
         self.device = self.refs.device
         self.struct = tq_page_pool(B, max_pages, num_pages, page_size, self.refs.data_ptr(),
                                    self.block_table.data_ptr(), self.lens.data_ptr())
+        self.ref = ctypes.byref(self.struct)
         tq_pages_workspace_bytes(self)  # checks the shape
 
 
@@ -669,7 +694,7 @@ def tq_page_arrays(caches) -> TQPageArrays:
 
 
 def tq_pages_workspace_bytes(pool: TQPagePool) -> int:
-    n = int(lib.tq_pages_workspace_bytes(ctypes.byref(pool.struct)))
+    n = int(lib.tq_pages_workspace_bytes(pool.ref))
     if n == 0:
         raise TQError(TQ_ERR_INVALID_ARG, last_error())
     return n
@@ -686,7 +711,7 @@ def _pool_arrays(pool: TQPagePool, arrays: TQPageArrays | None):
 def tq_pages_extend(pool: TQPagePool, need: torch.Tensor, status: torch.Tensor, stream=None) -> None:
     """lens[b] += need[b] (int32 [B]), with the lowest free pages. status (int32, one element): 0, or
     1 (not enough free pages) or 2 (a sequence would pass max_pages) and nothing changed."""
-    _run(lib.tq_pages_extend, pool.device, stream, ctypes.byref(pool.struct), _i32(need, pool.B, "need", pool.device),
+    _run(lib.tq_pages_extend, pool.device, stream, pool.ref, _i32(need, pool.B, "need", pool.device),
          _i32(status, -1, "status", pool.device))
 
 
@@ -695,14 +720,13 @@ def tq_pages_fork(pool: TQPagePool, arrays: TQPageArrays | None, parent_of: torc
     """Sequence b becomes a copy of sequence parent_of[b] (int32 [B]; -1: stays): full pages shared, a
     partly filled last page copied in all arrays."""
     ap, n = _pool_arrays(pool, arrays)
-    _run(lib.tq_pages_fork, pool.device, stream, ctypes.byref(pool.struct), ap, n,
-         _i32(parent_of, pool.B, "parent_of", pool.device), _i32(status, -1, "status", pool.device), _dev(ws, "ws"),
-         ws.numel() * ws.element_size())
+    _run(lib.tq_pages_fork, pool.device, stream, pool.ref, ap, n,
+         _i32(parent_of, pool.B, "parent_of", pool.device), _i32(status, -1, "status", pool.device), _ws(ws, pool.device), ws.nbytes)
 
 
 def tq_pages_free(pool: TQPagePool, leaving: torch.Tensor, stream=None) -> None:
     """Sequences with leaving[b] != 0 (int32 [B]) give their pages back."""
-    _run(lib.tq_pages_free, pool.device, stream, ctypes.byref(pool.struct),
+    _run(lib.tq_pages_free, pool.device, stream, pool.ref,
          _i32(leaving, pool.B, "leaving", pool.device))
 
 
@@ -710,8 +734,8 @@ def tq_pages_compact(pool: TQPagePool, arrays: TQPageArrays | None, live: torch.
                      stream=None) -> None:
     """Pack the live pages into the first ``live`` (int32, one element, written) pages of the pool."""
     ap, n = _pool_arrays(pool, arrays)
-    _run(lib.tq_pages_compact, pool.device, stream, ctypes.byref(pool.struct), ap, n,
-         _i32(live, -1, "live", pool.device), _dev(ws, "ws"), ws.numel() * ws.element_size())
+    _run(lib.tq_pages_compact, pool.device, stream, pool.ref, ap, n,
+         _i32(live, -1, "live", pool.device), _ws(ws, pool.device), ws.nbytes)
 
 
 def tq_pages_copy(arrays: TQPageArrays, src, dst, stream=None) -> None:

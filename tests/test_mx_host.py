@@ -204,7 +204,7 @@ def test_paged_cache_arrays_list_every_array_of_a_page():
 def test_bindings_refuse_host_tensors():
     with pytest.raises(tq.TQError):
         tq.TQMXCache(1, 1, 128, 16, 4, 4, torch.zeros(1, 4, dtype=torch.int32))
-    cache = type("C", (), dict(B=1, Hkv=1, d=128, device=torch.device("cuda", 0), struct=_mx(B=1, Hkv=1)))()
+    cache = type("C", (), dict(B=1, Hkv=1, d=128, device=torch.device("cuda", 0), ref=ctypes.byref(_mx(B=1, Hkv=1))))()
     x = torch.zeros(1, 1, 2, 128, dtype=torch.bfloat16)
     lens = torch.ones(1, dtype=torch.int32)
     for call in (lambda: tq.tq_quantize_kv_mx(x, None, cache, lens), lambda: tq.tq_dequantize_mx(cache, lens, x, x),
