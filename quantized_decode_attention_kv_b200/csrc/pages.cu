@@ -6,12 +6,13 @@
 // atomics are integer additions to reference counts. A call that cannot be carried out in full
 // changes nothing and says so in *status.
 //
-// The plan of a call (rank of every free or live page) is one launch of a cluster of 8 CTAs: each
-// warp counts its contiguous 1/256 of the reference counts, the CTA totals are exchanged through
-// distributed shared memory, and a second pass over the same (now cached) counts hands out ranks.
-// It is bound by launch and latency: a pool of 64 K pages is 256 KB of counts. Page contents move
-// as 16-byte vectors, 8 KB units flattened over (page, array) so that the small arrays of a page
-// do not leave CTAs idle; bound by HBM.
+// Bookkeeping of a call is one launch of one cluster: 1 CTA for pools of up to 16 K pages, 8 above
+// (64 KB of counts a pass; more CTAs only add barriers below that). Each warp counts its contiguous
+// share of the reference counts, the CTA totals are exchanged through distributed shared memory, and
+// a second look at the same counts (held as a bit mask a lane) hands out ranks. It is bound by
+// launch, memory latency and cold instructions, so its code is kept short. Page contents move as
+// 16-byte vectors, 8 KB units flattened over (page, array) so that the small arrays of a page do not
+// leave CTAs idle; bound by HBM.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -24,10 +25,11 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kCluster = 8;
+constexpr int kCluster = 8;         // CTAs of a plan for a large pool
+constexpr int kSmallPool = 1 << 14; // pages that one CTA plans
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
-constexpr int kSeqPer = kMaxPoolB / kPlanThreads; // sequences a thread of a plan owns
+constexpr long long kSmallTable = 1 << 14; // table entries whose rows a fork's plan writes itself
 constexpr int kCopyThreads = 128;
 constexpr int kCopyVecs = 4; // 16-byte vectors a thread moves at a time
 constexpr unsigned kChunk = kCopyThreads * kCopyVecs * 16;
@@ -50,129 +52,160 @@ struct CompactWs {
       : moves(static_cast<int *>(ws)), src(moves + 4), hole(src + pages), move_of(hole + pages) {}
 };
 
-__device__ __forceinline__ int pages_for(int len, int page_size) {
-  return (len + page_size - 1) / page_size; // len <= max_pages * page_size <= 2^30
-}
-
 struct PlanArgs {
   tq_page_pool p;
+  int shift;     // log2(page size)
   const int *in; // extend: positions to add; fork: parents
   int *status;   // extend, fork
   int *live;     // compact
   void *ws;
+  bool rows;     // fork, one CTA: the rows of the table too
 };
 
-// Inclusive scan over the CTA's threads; every thread gets its prefix and the total.
-__device__ __forceinline__ int block_scan(int v, int *s_warp, int &total) {
+__device__ __forceinline__ int pages_for(int len, int shift) { return (len + (1 << shift) - 1) >> shift; } // len <= 2^30
+
+// A child's new row of the table, from the table as it was, and its old pages given back.
+__device__ __forceinline__ void gather_row(const tq_page_pool &p, int shift, const ForkWs &f, int b, int from, int step) {
+  const int par = f.parent[b];
+  if (par < 0) return;
+  const int n = pages_for(f.len[b], shift);
+  const long long row = static_cast<long long>(b) * p.max_pages;
+  for (int j = from; j < p.max_pages; j += step) {
+    const int old = p.block_table[row + j];
+    if (old >= 0 && old < p.num_pages) atomicSub(p.refs + old, 1);
+    f.rows[row + j] = j < n ? p.block_table[static_cast<long long>(par) * p.max_pages + j] : -1;
+  }
+}
+// Writes the row, its length and its counts.
+__device__ __forceinline__ void apply_row(const tq_page_pool &p, int shift, const ForkWs &f, int b, int from, int step) {
+  if (f.parent[b] < 0) return;
+  const long long row = static_cast<long long>(b) * p.max_pages;
+  const int fresh = f.fresh[b], len = f.len[b];
+  for (int j = from; j < p.max_pages; j += step) {
+    int e = f.rows[row + j];
+    if (fresh >= 0 && j == len >> shift) e = fresh; // counted when it was handed out
+    else if (e >= 0 && e < p.num_pages) atomicAdd(p.refs + e, 1);
+    p.block_table[row + j] = e;
+    if (j == 0) p.lens[b] = len;
+  }
+}
+
+// Prefix of a thread's number over the CTA's threads (those before it) and the total.
+__device__ __forceinline__ unsigned block_scan(unsigned v, unsigned *s_warp, unsigned &total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned incl = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
+    const unsigned u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
   }
+  __syncthreads(); // the readers of the scan before are done
+  if (lane == 31) s_warp[warp] = incl;
   __syncthreads();
-  if (lane == 31) s_warp[warp] = v;
-  __syncthreads();
-  int before = 0;
-  total = 0;
-  for (int w = 0; w < kPlanWarps; ++w) {
-    if (w < warp) before += s_warp[w];
-    total += s_warp[w];
+  unsigned w = s_warp[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned u = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += u;
   }
-  return before + v;
+  total = __shfl_sync(0xffffffffu, w, 31);
+  return (warp ? __shfl_sync(0xffffffffu, w, warp - 1) : 0u) + incl - v;
 }
 
 template <int MODE>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
-  __shared__ int s_pre[MODE == kCompact ? 1 : kMaxPoolB]; // pages handed to the sequences before this one
-  __shared__ int s_had[MODE == kExtend ? kMaxPoolB : 1];  // pages the sequence had
-  __shared__ int s_warp[kPlanWarps];
-  __shared__ int s_total; // this CTA's count, read by the others
-  __shared__ int s_long; // a sequence would pass its row of the table
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
+  __shared__ unsigned s_pre[MODE == kCompact ? 1 : kMaxPoolB]; // pages handed to the sequences before this one
+  __shared__ int s_had[MODE == kExtend ? kMaxPoolB : 1];       // pages the sequence had
+  __shared__ unsigned s_warp[kPlanWarps];
+  __shared__ unsigned s_total; // this CTA's count, read by the others
+  __shared__ int s_long;       // a sequence would pass its row of the table
   __shared__ unsigned long long s_sum;
   cg::cluster_group cluster = cg::this_cluster();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = cluster.block_rank();
-  const int B = a.p.B, ps = a.p.page_size, pages = a.p.num_pages, cap = a.p.max_pages * ps;
-  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = cluster.block_rank(), ctas = cluster.num_blocks();
+  const int B = a.p.B, pages = a.p.num_pages, cap = a.p.max_pages << a.shift;
   if (tid == 0) s_long = 0, s_sum = 0;
-  __syncthreads();
-  // ---- what each sequence needs (every CTA computes all of it)
-  int wanted = 0;
-  if constexpr (MODE != kCompact) {
-    ForkWs f(a.ws, B);
-    int need[kSeqPer], sum = 0;
-#pragma unroll
-    for (int i = 0; i < kSeqPer; ++i) {
-      const int b = tid * kSeqPer + i;
-      need[i] = 0;
-      if (b >= B) continue;
-      if constexpr (MODE == kExtend) {
-        const int len = max(a.p.lens[b], 0);
-        const long long after = static_cast<long long>(len) + max(a.in[b], 0);
-        if (after > cap) s_long = 1;
-        else need[i] = pages_for(static_cast<int>(after), ps) - pages_for(len, ps);
-        s_had[b] = len <= cap ? pages_for(len, ps) : 0;
-      } else {
-        const int par = a.in[b];
-        const bool valid = par >= 0 && par < B && par != b;
-        const int len = valid ? min(max(a.p.lens[par], 0), cap) : 0;
-        need[i] = len % ps != 0;
-        if (rank == 0) f.parent[b] = valid ? par : -1, f.len[b] = len, f.fresh[b] = -1;
-      }
-      sum += need[i]; // at most 4 * 2^26
-    }
-    const int incl = block_scan(sum, s_warp, wanted);
-    atomicAdd(&s_sum, static_cast<unsigned long long>(sum)); // the scan itself may wrap; then the call fails
-    int run = incl - sum;
-#pragma unroll
-    for (int i = 0; i < kSeqPer; ++i) {
-      const int b = tid * kSeqPer + i;
-      if (b < B) s_pre[b] = run;
-      run += need[i];
-    }
-  }
-  // ---- count the free (compact: live) pages of this warp's part of the pool
-  const int part = ((pages + kCluster * kPlanWarps - 1) / (kCluster * kPlanWarps) + 127) / 128 * 128;
-  const long long begin = static_cast<long long>(rank * kPlanWarps + warp) * part;
+  pdl_wait();
+  // ---- the free (compact: live) pages of this warp's share of the pool: four adjacent ones a lane and
+  // step, 128 a warp; the first eight steps' as a bit mask
+  const int share = ((pages + ctas * kPlanWarps - 1) / (ctas * kPlanWarps) + 127) / 128 * 128;
+  const long long begin = static_cast<long long>(rank * kPlanWarps + warp) * share;
   const int lo = static_cast<int>(min(begin, static_cast<long long>(pages)));
-  const int hi = static_cast<int>(min(begin + part, static_cast<long long>(pages)));
-  auto load = [&](int i, bool (&hit)[4]) { // pages i .. i + 3 (i a multiple of 4)
+  const int hi = static_cast<int>(min(begin + share, static_cast<long long>(pages)));
+  auto look = [&](int i) -> unsigned { // bits for pages i .. i + 3 (i a multiple of 4)
+    if (i >= hi) return 0u;
     int r[4] = {1, 1, 1, 1};
+    unsigned valid = 15u;
     if (i + 4 <= pages) {
       const int4 v = *reinterpret_cast<const int4 *>(a.p.refs + i);
       r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
     } else {
-      for (int e = 0; e < 4; ++e)
-        if (i + e < pages) r[e] = a.p.refs[i + e];
+      valid = (1u << (pages - i)) - 1u;
+      for (int e = 0; i + e < pages; ++e) r[e] = a.p.refs[i + e];
     }
-    for (int e = 0; e < 4; ++e) hit[e] = i + e < pages && (MODE == kCompact ? r[e] != 0 : r[e] == 0);
+    const unsigned zero = (r[0] == 0) | (r[1] == 0) << 1 | (r[2] == 0) << 2 | (r[3] == 0) << 3;
+    return (MODE == kCompact ? ~zero : zero) & valid;
   };
-  int cnt = 0;
-  for (int i = lo + lane * 4; i < hi; i += 128) {
-    bool hit[4];
-    load(i, hit);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) cnt += hit[e];
+  unsigned held = 0; // the first eight looks
+  unsigned cnt = 0;
+#pragma unroll 1
+  for (int i = lo + lane * 4, n = 0; i < hi; i += 128, ++n) {
+    const unsigned m = look(i);
+    if (n < 8) held |= m << (4 * n);
+    cnt += __popc(m);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) cnt += __shfl_xor_sync(0xffffffffu, cnt, o);
-  __syncthreads(); // block_scan's readers of s_warp are done
-  if (lane == 0) s_warp[warp] = cnt;
-  __syncthreads();
-  if (tid == 0) {
-    int t = 0;
-    for (int w = 0; w < kPlanWarps; ++w) t += s_warp[w];
-    s_total = t;
+  cnt = __reduce_add_sync(0xffffffffu, cnt);
+  // ---- what each sequence needs (every CTA computes all of it)
+  unsigned wanted = 0;
+  if constexpr (MODE != kCompact) {
+    const ForkWs f(a.ws, B);
+    const int per = (B + kPlanThreads - 1) / kPlanThreads;
+    auto need_of = [&](int b, int &had) -> unsigned {
+      if constexpr (MODE == kExtend) {
+        const int len = max(a.p.lens[b], 0);
+        const long long after = static_cast<long long>(len) + max(a.in[b], 0);
+        had = len <= cap ? pages_for(len, a.shift) : 0;
+        if (after > cap) {
+          s_long = 1;
+          return 0u;
+        }
+        return pages_for(static_cast<int>(after), a.shift) - had;
+      } else {
+        const int par = a.in[b];
+        const bool valid = static_cast<unsigned>(par) < static_cast<unsigned>(B) && par != b;
+        const int len = valid ? min(max(a.p.lens[par], 0), cap) : 0;
+        if (rank == 0) f.parent[b] = valid ? par : -1, f.len[b] = len, f.fresh[b] = -1;
+        return (len & ((1 << a.shift) - 1)) != 0;
+      }
+    };
+    unsigned sum = 0; // at most 4 * 2^26
+    int had = 0;
+#pragma unroll 1
+    for (int b = tid * per; b < min(B, (tid + 1) * per); ++b) sum += need_of(b, had);
+    unsigned run = block_scan(sum, s_warp, wanted);
+    if (sum) atomicAdd(&s_sum, static_cast<unsigned long long>(sum)); // the scan may wrap; then the call fails
+#pragma unroll 1
+    for (int b = tid * per; b < min(B, (tid + 1) * per); ++b) {
+      const unsigned need = need_of(b, had);
+      s_pre[b] = run;
+      if constexpr (MODE == kExtend) s_had[b] = had;
+      run += need;
+    }
   }
-  cluster.sync(); // totals are visible; every CTA has read lens and its part of refs
-  int before = 0, all = 0;
-  for (int r = 0; r < kCluster; ++r) {
-    const int t = *cluster.map_shared_rank(&s_total, r);
-    if (r < rank) before += t;
-    all += t;
+  unsigned all, before = block_scan(lane == 0 ? cnt : 0u, s_warp, all); // every lane of a warp: the warps before it
+  before = __shfl_sync(0xffffffffu, before, 0);
+  if (ctas > 1) {
+    if (tid == 0) s_total = all;
+    cluster.sync(); // totals are visible; every CTA has read lens and its part of refs
+    all = 0;
+    for (int r = 0; r < ctas; ++r) {
+      const unsigned t = *cluster.map_shared_rank(&s_total, r);
+      if (r < rank) before += t;
+      all += t;
+    }
+    cluster.sync(); // nobody leaves while its total is being read
+  } else {
+    __syncthreads();
   }
-  cluster.sync(); // nobody leaves while its total is being read
-  for (int w = 0; w < warp; ++w) before += s_warp[w];
   if constexpr (MODE != kCompact) {
     const int status = s_long ? 2 : s_sum > static_cast<unsigned long long>(all) ? 1 : 0;
     if (rank == 0 && tid == 0) {
@@ -180,63 +213,71 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
       if constexpr (MODE == kFork) ForkWs(a.ws, B).state[0] = status;
     }
     if (status != 0) return;
-  }
-  if constexpr (MODE == kCompact) {
-    if (rank == 0 && tid == 0) {
-      *a.live = all;
-      if (all == pages) *CompactWs(a.ws, pages).moves = 0;
-    }
+  } else if (rank == 0 && tid == 0) {
+    *a.live = static_cast<int>(all);
+    if (static_cast<int>(all) == pages) *CompactWs(a.ws, pages).moves = 0;
   }
   // ---- hand out the ranks
-  for (int i0 = lo; i0 < hi; i0 += 128) {
+#pragma unroll 1
+  for (int i0 = lo, n = 0; i0 < hi; i0 += 128, ++n) {
     if (MODE != kCompact && before >= wanted) break;
     const int i = i0 + lane * 4;
-    bool hit[4] = {false, false, false, false};
-    if (i < hi) load(i, hit);
-    int sum = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) sum += hit[e];
-    int incl = sum;
+    const unsigned hit = n < 8 ? held >> (4 * n) & 15u : look(i);
+    unsigned incl = __popc(hit);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, incl, o);
+      const unsigned u = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += u;
     }
-    int k = before + incl - sum; // free (live) pages before this one
+    unsigned k = before + incl - __popc(hit); // free (live) pages before this one
     before += __shfl_sync(0xffffffffu, incl, 31);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int page = i + e;
-      if constexpr (MODE == kCompact) {
-        if (page >= pages || i >= hi) continue;
-        CompactWs c(a.ws, pages);
-        if (page == all) *c.moves = all - k;
-        if (page < all) {
-          if (!hit[e]) c.hole[page - k] = page;
+    if constexpr (MODE == kCompact) {
+      const CompactWs c(a.ws, pages);
+      const int live = static_cast<int>(all);
+#pragma unroll 1
+      for (int page = i; page < min(i + 4, hi); ++page) {
+        const bool is = hit >> (page - i) & 1u;
+        if (page == live) *c.moves = live - static_cast<int>(k);
+        if (page < live) {
+          if (!is) c.hole[page - k] = page;
         } else {
-          const int m = all - 1 - k; // live pages above this one
-          if (hit[e]) c.src[m] = page;
-          c.move_of[page] = hit[e] ? m : -1;
+          const int m = live - 1 - static_cast<int>(k); // live pages above this one
+          if (is) c.src[m] = page;
+          c.move_of[page] = is ? m : -1;
         }
-        k += hit[e];
-      } else {
-        if (hit[e] && k < wanted) {
-          int b0 = 0, b1 = B; // the last sequence with s_pre <= k
-          while (b1 - b0 > 1) {
-            const int mid = (b0 + b1) >> 1;
-            (s_pre[mid] <= k ? b0 : b1) = mid;
-          }
-          if constexpr (MODE == kExtend)
-            a.p.block_table[static_cast<long long>(b0) * a.p.max_pages + s_had[b0] + (k - s_pre[b0])] = page;
-          else
-            ForkWs(a.ws, B).fresh[b0] = page;
-          a.p.refs[page] = 1;
+        k += is;
+      }
+    } else {
+#pragma unroll 1
+      for (unsigned left = hit; left && k < wanted; left &= left - 1, ++k) {
+        const int page = i + __ffs(left) - 1;
+        int b0 = 0, b1 = B; // the last sequence with s_pre <= k
+#pragma unroll 1
+        while (b1 - b0 > 1) {
+          const int mid = (b0 + b1) >> 1;
+          (s_pre[mid] <= k ? b0 : b1) = mid;
         }
-        k += hit[e];
+        if constexpr (MODE == kExtend)
+          a.p.block_table[static_cast<long long>(b0) * a.p.max_pages + s_had[b0] + (k - s_pre[b0])] = page;
+        else
+          ForkWs(a.ws, B).fresh[b0] = page;
+        a.p.refs[page] = 1;
       }
     }
   }
+  if constexpr (MODE == kFork) {
+    if (a.rows) {
+      __syncthreads(); // parents, lengths and fresh pages are there
+      const ForkWs f(a.ws, B);
+#pragma unroll 1
+      for (int b = warp; b < B; b += kPlanWarps) gather_row(a.p, a.shift, f, b, lane, 32);
+      __syncthreads(); // every row has been read
+#pragma unroll 1
+      for (int b = warp; b < B; b += kPlanWarps) apply_row(a.p, a.shift, f, b, lane, 32);
+    }
+  }
   if (MODE == kExtend && rank == 0) { // every CTA has read lens (first cluster barrier)
+#pragma unroll 1
     for (int b = tid; b < B; b += kPlanThreads) a.p.lens[b] = max(a.p.lens[b], 0) + max(a.in[b], 0);
   }
 }
@@ -289,51 +330,30 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
 }
 
 // ---------------------------------------------------------------- fork
-// The new rows, from the table as it was, and the children's old pages given back.
-__global__ void __launch_bounds__(256) fork_rows_kernel(const tq_page_pool p, void *ws) {
+__global__ void __launch_bounds__(256) fork_rows_kernel(const tq_page_pool p, int shift, void *ws) {
   pdl_wait();
-  ForkWs f(ws, p.B);
+  const ForkWs f(ws, p.B);
   if (f.state[0] != 0) return;
-  for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
-    const int par = f.parent[b];
-    if (par < 0) continue;
-    const int n = pages_for(f.len[b], p.page_size);
-    const long long row = static_cast<long long>(b) * p.max_pages;
-    for (int j = blockIdx.x * 256 + threadIdx.x; j < p.max_pages; j += gridDim.x * 256) {
-      const int old = p.block_table[row + j];
-      if (old >= 0 && old < p.num_pages) atomicSub(p.refs + old, 1);
-      f.rows[row + j] = j < n ? p.block_table[static_cast<long long>(par) * p.max_pages + j] : -1;
-    }
-  }
+  for (int b = blockIdx.y; b < p.B; b += gridDim.y)
+    gather_row(p, shift, f, b, blockIdx.x * 256 + threadIdx.x, gridDim.x * 256);
 }
 
-// Blocks of y = 0 write the table, lengths and counts; those of y = 1 copy the partial pages.
+// Blocks of y = 0 write the table, lengths and counts; those of y = 1 (first: 0) copy the partial pages.
 template <int N>
-__global__ void __launch_bounds__(kCopyThreads) fork_apply_kernel(const tq_page_pool p,
+__global__ void __launch_bounds__(kCopyThreads) fork_apply_kernel(const tq_page_pool p, int shift, int first,
                                                                   const __grid_constant__ Arrays<N> ar, void *ws) {
   pdl_wait();
-  ForkWs f(ws, p.B);
+  const ForkWs f(ws, p.B);
   if (f.state[0] != 0) return;
-  if (blockIdx.y == 0) {
-    const int across = (p.max_pages + kCopyThreads - 1) / kCopyThreads;
-    for (long long w = blockIdx.x; w < static_cast<long long>(across) * p.B; w += gridDim.x) {
-      const int b = static_cast<int>(w / across), j = static_cast<int>(w - static_cast<long long>(b) * across) * kCopyThreads + threadIdx.x;
-      if (f.parent[b] < 0 || j >= p.max_pages) continue;
-      const long long row = static_cast<long long>(b) * p.max_pages;
-      const int fresh = f.fresh[b], len = f.len[b];
-      int e = f.rows[row + j];
-      if (fresh >= 0 && j == len / p.page_size) e = fresh; // counted when it was handed out
-      else if (e >= 0 && e < p.num_pages) atomicAdd(p.refs + e, 1);
-      p.block_table[row + j] = e;
-      if (j == 0) p.lens[b] = len;
-    }
+  if (static_cast<int>(blockIdx.y) + first == 0) {
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) apply_row(p, shift, f, b, threadIdx.x, kCopyThreads);
     return;
   }
   for (long long w = blockIdx.x; w < static_cast<long long>(p.B) * ar.units; w += gridDim.x) {
     const int b = static_cast<int>(w / ar.units);
     const int fresh = f.fresh[b];
     if (fresh < 0) continue;
-    const int src = f.rows[static_cast<long long>(b) * p.max_pages + f.len[b] / p.page_size];
+    const int src = f.rows[static_cast<long long>(b) * p.max_pages + (f.len[b] >> shift)];
     if (src < 0 || src >= p.num_pages) continue;
     move_unit(ar, static_cast<unsigned>(w - static_cast<long long>(b) * ar.units), src, fresh);
   }
@@ -408,6 +428,29 @@ cudaError_t with_arrays(const tq_page_array *arrays, int n, F &&f) {
   return n <= kFewArrays ? f(pack<kFewArrays>(arrays, n)) : f(pack<kMaxPageArrays>(arrays, n));
 }
 
+int shift_of(const tq_page_pool &p) {
+  int n = 0;
+  while ((1 << n) < p.page_size) ++n;
+  return n;
+}
+
+cudaError_t launch_plan(void (*kernel)(PlanArgs), cudaStream_t s, const PlanArgs &a) {
+  const unsigned ctas = a.p.num_pages <= kSmallPool ? 1 : kCluster;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 dim3 row_grid(const tq_page_pool &p) {
   return dim3(static_cast<unsigned>(std::min((p.max_pages + 255) / 256, 64)), static_cast<unsigned>(p.B));
 }
@@ -421,21 +464,25 @@ size_t pages_workspace_bytes(const tq_page_pool &p) {
 }
 
 cudaError_t launch_pages_extend(const tq_page_pool &p, const int *need, int *status, cudaStream_t s) {
-  return launch_pdl(plan_kernel<kExtend>, dim3(kCluster), dim3(kPlanThreads), 0, s,
-                    PlanArgs{p, need, status, nullptr, nullptr});
+  return launch_plan(plan_kernel<kExtend>, s, PlanArgs{p, shift_of(p), need, status, nullptr, nullptr, false});
 }
 
 cudaError_t launch_pages_fork(const tq_page_pool &p, const tq_page_array *arrays, int n_arrays,
                               const int *parent_of, int *status, void *ws, int sm_count, cudaStream_t s) {
-  cudaError_t e = launch_pdl(plan_kernel<kFork>, dim3(kCluster), dim3(kPlanThreads), 0, s,
-                             PlanArgs{p, parent_of, status, nullptr, ws});
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(fork_rows_kernel, row_grid(p), dim3(256), 0, s, p, ws);
-  if (e != cudaSuccess) return e;
+  // One CTA also gathers and writes a small table's rows: 16 K entries are 16 steps of its threads, less
+  // than a launch (3.5 us on the host); above that the rows go over the GPU.
+  const bool rows = p.num_pages <= kSmallPool && static_cast<long long>(p.B) * p.max_pages <= kSmallTable;
+  cudaError_t e = launch_plan(plan_kernel<kFork>, s, PlanArgs{p, shift_of(p), parent_of, status, nullptr, ws, rows});
+  if (e != cudaSuccess || (rows && n_arrays == 0)) return e;
+  if (!rows) {
+    e = launch_pdl(fork_rows_kernel, row_grid(p), dim3(256), 0, s, p, shift_of(p), ws);
+    if (e != cudaSuccess) return e;
+  }
   return with_arrays(arrays, n_arrays, [&](const auto &ar) {
     using A = std::decay_t<decltype(ar)>;
     constexpr int N = sizeof(A) > sizeof(Arrays<kFewArrays>) ? kMaxPageArrays : kFewArrays;
-    return launch_pdl(fork_apply_kernel<N>, dim3(sm_count * 8, n_arrays ? 2 : 1), dim3(kCopyThreads), 0, s, p, ar, ws);
+    const dim3 grid(sm_count * 8, (n_arrays > 0) + !rows);
+    return launch_pdl(fork_apply_kernel<N>, grid, dim3(kCopyThreads), 0, s, p, shift_of(p), static_cast<int>(rows), ar, ws);
   });
 }
 
@@ -445,8 +492,7 @@ cudaError_t launch_pages_free(const tq_page_pool &p, const int *leaving, cudaStr
 
 cudaError_t launch_pages_compact(const tq_page_pool &p, const tq_page_array *arrays, int n_arrays, int *live,
                                  void *ws, int sm_count, cudaStream_t s) {
-  cudaError_t e = launch_pdl(plan_kernel<kCompact>, dim3(kCluster), dim3(kPlanThreads), 0, s,
-                             PlanArgs{p, nullptr, nullptr, live, ws});
+  cudaError_t e = launch_plan(plan_kernel<kCompact>, s, PlanArgs{p, shift_of(p), nullptr, nullptr, live, ws, false});
   if (e != cudaSuccess) return e;
   return with_arrays(arrays, n_arrays, [&](const auto &ar) {
     using A = std::decay_t<decltype(ar)>;

@@ -225,7 +225,7 @@ cudaError_t launch_mx_decode(const MxDecodeArgs &a, cudaStream_t s);
 // ---------------------------------------------------------------- pages of paged caches
 constexpr int kMaxPoolB = 4096;       // sequences of a page pool
 constexpr int kMaxPageArrays = 1024;  // arrays (over all layers) that one call moves pages of
-constexpr int kPageCopyBatch = 512;   // (source, destination) pairs in one launch's parameters
+constexpr int kPageCopyBatch = 256;   // (source, destination) pairs in one launch's parameters
 
 cudaError_t launch_pages_extend(const tq_page_pool &p, const int *need, int *status, cudaStream_t s);
 cudaError_t launch_pages_fork(const tq_page_pool &p, const tq_page_array *arrays, int n_arrays,

@@ -7,6 +7,7 @@ fallback path.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from dataclasses import dataclass
@@ -738,13 +739,27 @@ def tq_pages_compact(pool: TQPagePool, arrays: TQPageArrays | None, live: torch.
          _i32(live, -1, "live", pool.device), _ws(ws, pool.device), ws.nbytes)
 
 
+def _host_ints(x, name: str):
+    """A list or integer array of host integers as C ints: (owner of the memory, address)."""
+    try:
+        if isinstance(x, list):
+            a = array.array("i", x)
+            return a, a.buffer_info()[0]
+        a = np.asarray(x)
+        if a.ndim != 1 or a.dtype.kind not in "iu" or (a.size and (a.min() < -2 ** 31 or a.max() >= 2 ** 31)):
+            raise ValueError("not a one-dimensional list of C ints")
+        a = np.ascontiguousarray(a, dtype=np.int32)
+        return a, a.ctypes.data
+    except (TypeError, ValueError, OverflowError) as e:
+        raise TQError(TQ_ERR_INVALID_ARG, f"{name} must be a list of page numbers: {e}") from None
+
+
 def tq_pages_copy(arrays: TQPageArrays, src, dst, stream=None) -> None:
     """Copy pages src[i] to dst[i] (host integers) in all arrays; dst distinct and none of them a src."""
-    s, t = (np.ascontiguousarray(x, dtype=np.int32) for x in (src, dst))
-    if s.ndim != 1 or s.shape != t.shape:
-        raise TQError(TQ_ERR_INVALID_ARG, "src and dst must be equally long lists of page numbers")
-    _run(lib.tq_pages_copy, arrays.device, stream, arrays.arrays, arrays.n, arrays.num_pages, s.ctypes.data,
-         t.ctypes.data, s.shape[0])
+    (s, sp), (t, tp) = _host_ints(src, "src"), _host_ints(dst, "dst")  # s and t keep the memory until the call is over
+    if len(s) != len(t):
+        raise TQError(TQ_ERR_INVALID_ARG, f"src and dst must be equally long, got {len(s)} and {len(t)} pages")
+    _run(lib.tq_pages_copy, arrays.device, stream, arrays.arrays, arrays.n, arrays.num_pages, sp, tp, len(s))
 
 
 def workspace(nbytes: int, device="cuda") -> torch.Tensor:

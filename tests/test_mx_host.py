@@ -212,3 +212,16 @@ def test_bindings_refuse_host_tensors():
                  lambda: tq.tq_decode_attention_mx(x, cache, lens, 0.1, x, x)):
         with pytest.raises(tq.TQError):
             call()
+
+
+@pytest.mark.parametrize("bad", [[2 ** 32], [1.5], [[1, 2]], np.array([0.0]), np.array([2 ** 33]), np.zeros((1, 1), int), ["1"]])
+def test_page_lists_that_are_no_c_ints_are_refused(bad):
+    with pytest.raises(tq.TQError):
+        tq._host_ints(bad, "src")
+
+
+def test_page_lists_of_any_integer_type():
+    for x in ([3, 1], (3, 1), np.array([3, 1]), np.array([3, 9, 1, 9], np.uint8)[::2], torch.tensor([3, 1])):
+        owner, address = tq._host_ints(x, "src")
+        assert len(owner) == 2 and list((ctypes.c_int * 2).from_address(address)) == [3, 1]
+    assert len(tq._host_ints([], "src")[0]) == 0 and len(tq._host_ints(np.array([], int), "src")[0]) == 0
