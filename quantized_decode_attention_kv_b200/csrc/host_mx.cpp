@@ -100,6 +100,7 @@ int check_rows(const void *K, const void *V, int dtype, int T, const int32_t *le
     return fail(TQ_ERR_INVALID_ARG, "lens must be non-NULL, lens and counts 4-byte aligned");
   a->x[0] = const_cast<void *>(K);
   a->x[1] = const_cast<void *>(V);
+  for (int i = 0; i < 2; ++i) a->inv6g[i] = 1.0f / (6.0f * a->c.g[i]);
   a->dtype = dtype;
   a->T = T;
   a->lens = lens;

@@ -196,6 +196,7 @@ struct MxCacheArgs {
 struct MxRowsArgs { // write (x -> pages) or read (pages -> x) of up to T rows of each sequence
   MxCacheArgs c;
   void *x[2];          // keys, values (NULL: skipped)
+  float inv6g[2];      // 1 / (6 g), rounded
   long long st[2][3];  // strides of x in elements: sequence, head, row
   int dtype, T;
   const int *lens, *counts;
