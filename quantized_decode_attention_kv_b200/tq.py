@@ -588,7 +588,7 @@ def _mx_strides(x, name: str):
     s = x.stride()
     if s[3] != 1:
         raise TQError(TQ_ERR_INVALID_ARG, f"{name}: the elements of a row must be adjacent")
-    return x.data_ptr(), (ctypes.c_int64 * 3)(*s[:3])
+    return x.data_ptr(), (ctypes.c_int64 * 3)(*(0 if n == 1 else i for n, i in zip(x.shape, s[:3])))
 
 
 def tq_quantize_kv_mx(K: torch.Tensor | None, V: torch.Tensor | None, cache: TQMXCache, lens: torch.Tensor,

@@ -135,6 +135,88 @@ def test_write_takes_the_slices_of_a_fused_projection():
     assert (c["v_codes"] == 0).all()  # V was None
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("g", [1.0, 2.0 ** -7, 0.75])  # 0.75: not a power of two, S g still exact in fp32
+def test_every_16_bit_value_at_every_scale_rounds_right(dtype, g):
+    # blocks of fifteen values and one that sets the scale to S = 1 + m / 8: all finite patterns up to it,
+    # of both signs
+    t = DT[dtype]
+    every = torch.arange(0x7C00 if dtype == "f16" else 0x7F80, dtype=torch.int32).to(torch.int16).view(t).double()
+    rows = []
+    for m in range(8):
+        top = 6.0 * (1 + m / 8) * g
+        assert float(torch.tensor(top, dtype=t)) == top
+        v = every[(every <= top) & (every >= top / 4096)]  # smaller ones are far below the first midpoint
+        v = torch.cat([v, -v, torch.zeros(-2 * len(v) % 15, dtype=torch.float64)]).view(-1, 15)
+        rows.append(torch.cat([v, torch.full((len(v), 1), top, dtype=torch.float64)], dim=1))
+    x = torch.cat(rows)
+    x = torch.cat([x, torch.zeros(-len(x) % 4, 16, dtype=torch.float64)]).view(1, 1, -1, 64).to(t)
+    T = x.shape[2]
+    cache = _cache(1, 1, 64, 64, -(-T // 64), g=(g, g))
+    tq.tq_quantize_kv_mx(x.cuda(), None, cache, _i32([T]))
+    codes, s = M.quantise(_np(x[0, 0]), g)
+    got_c, got_s = _records(cache, "k", 0, 0, np.arange(T))
+    np.testing.assert_array_equal(got_s, s)
+    np.testing.assert_array_equal(M.values(got_c, s, g), M.values(M.pack(codes), s, g))
+
+
+@pytest.mark.parametrize("d,dtype,B,Hkv,T,page,layout", [
+    (128, "bf16", 2, 3, 200, 16, "heads"),     # two rows a thread
+    (128, "f16", 8, 8, 641, 64, "rows"),       # four rows a thread, ragged end
+    (64, "f32", 8, 8, 1300, 32, "heads"),
+    (256, "bf16", 8, 8, 330, 16, "rows"),
+    (64, "f16", 1, 1, 129, 128, "rows"),
+])
+def test_bulk_calls_equal_calls_of_few_rows(d, dtype, B, Hkv, T, page, layout):
+    """Whole prompts at once, from both layouts, one side or both: the bytes of calls of 16 rows each
+    (which the oracle's tests cover), and the same rows back."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    shape = (B, T, Hkv, d) if layout == "heads" else (B, Hkv, T, d)
+    K, V = (torch.randn(shape, generator=g, device="cuda").to(DT[dtype]) for _ in range(2))
+    if layout == "heads":  # a model's [sequence][row][head] layout
+        K, V = K.transpose(1, 2), V.transpose(1, 2)
+    counts = [T] + [T - 1 - (37 * b) % T for b in range(1, B)]
+    lens = [n + 5 * b for b, n in enumerate(counts)]
+    max_pages = -(-max(lens) // page)
+    a, b_, c = (_cache(B, Hkv, d, page, max_pages, g=(0.5, 2.0), seed=T) for _ in range(3))
+    for cache in (a, b_, c):
+        _fill(cache, 0x3C)
+    tq.tq_quantize_kv_mx(K, V, a, _i32(lens), _i32(counts))
+    tq.tq_quantize_kv_mx(K, None, b_, _i32(lens), _i32(counts))
+    tq.tq_quantize_kv_mx(None, V, b_, _i32(lens), _i32(counts))
+    for t in range(0, T, 16):
+        n = min(16, T - t)
+        now = [min(max(k - t, 0), n) for k in counts]
+        tq.tq_quantize_kv_mx(K[:, :, t:t + n], V[:, :, t:t + n], c, _i32([L - k + t + m for L, k, m in zip(lens, counts, now)]),
+                             _i32(now))
+    for key in a.tensors:
+        assert torch.equal(a[key], c[key]) and torch.equal(b_[key], c[key])
+    for out_t in DT.values():
+        big, few = ([torch.full((B, Hkv, T, d), 9.0, dtype=out_t, device="cuda") for _ in range(2)] for _ in range(2))
+        tq.tq_dequantize_mx(a, _i32(lens), *big, _i32(counts))
+        only = torch.full_like(big[1], 9.0)
+        tq.tq_dequantize_mx(a, _i32(lens), None, only, _i32(counts))
+        assert torch.equal(only, big[1])
+        for t in range(0, T, 16):
+            n = min(16, T - t)
+            now = [min(max(k - t, 0), n) for k in counts]
+            part = [torch.empty((B, Hkv, n, d), dtype=out_t, device="cuda") for _ in range(2)]
+            tq.tq_dequantize_mx(a, _i32([L - k + t + m for L, k, m in zip(lens, counts, now)]), *part, _i32(now))
+            for f, p in zip(few, part):
+                f[:, :, t:t + n] = p
+        assert all(torch.equal(x, y) for x, y in zip(big, few))
+
+
+def test_strides_of_single_rows_and_sequences_do_not_matter():
+    cache, other = _cache(1, 2, 64, 16, 2), _cache(1, 2, 64, 16, 2)
+    base = _randn((2 * 64 + 7 + 3 * 64,), torch.bfloat16, 77).cuda()
+    x = base.as_strided((1, 2, 1, 64), (7, 128, 3, 1))  # strides of size-1 dimensions that are no multiples of 16 bytes
+    tq.tq_quantize_kv_mx(x, x, cache, _i32([5]))
+    tq.tq_quantize_kv_mx(x.contiguous(), x.contiguous(), other, _i32([5]))
+    for key in cache.tensors:
+        assert torch.equal(cache[key], other[key])
+
+
 @pytest.mark.parametrize("dtype", list(DT))
 def test_write_of_special_values(dtype):
     t = DT[dtype]
@@ -264,6 +346,10 @@ def _check(cache, q, lens, counts=None, scale=None, out_dtype=None):
     (128, 2, 4, 5, 16, [100, 5, 47, 16], "bf16", "f32"),       # 20 rows in two blocks of 16
     (128, 1, 8, 16, 32, [64, 16, 200], "f16", "f32"),          # 128 rows in eight blocks
     (64, 1, 7, 2, 16, [31, 33], "f16", "bf16"),
+    (64, 2, 6, 4, 32, [120, 33, 4, 64], "bf16", "f32"),        # 24 rows: three column tiles
+    (128, 1, 11, 2, 16, [15, 16, 17, 31, 32, 33, 48, 65], "bf16", "f16"),  # 22 rows, ends within a step of 32
+    (64, 3, 2, 1, 64, [15, 16, 17, 31, 32, 33, 48, 63, 65, 96], "f16", "f32"),
+    (256, 2, 8, 1, 128, [1000, 31, 130], "f16", "f32"),
     (128, 8, 4, 1, 64, [3000], "bf16", "f32"),                 # few units, many CTAs each
     (64, 1, 1, 1, 16, [20000], "bf16", "f32"),                 # one unit over all CTAs
     (128, 4, 4, 1, 16, [7] * 100, "bf16", "f32"),              # many units, one tile each

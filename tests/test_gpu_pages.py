@@ -83,6 +83,24 @@ def test_a_random_life_matches_the_oracle(B, max_pages, num_pages, page, layers)
     assert 0 in seen or B == 1
 
 
+@pytest.mark.parametrize("B,max_pages,num_pages", [(24, 3000, 40_000), (700, 900, 400_003)])
+def test_large_pools_are_planned_by_several_blocks(B, max_pages, num_pages):
+    # more pages than one block plans, and (400 003) more than its bit masks hold
+    rng = np.random.default_rng(num_pages)
+    w = Both(B, max_pages, num_pages, 16, layers=0)
+    for refs in (w.pool.refs, w.want.refs):  # pages held by others all over the pool
+        refs[::7] = 3
+    seen = set()
+    for step in range(3):
+        seen.add(w.extend(rng.integers(0, max_pages * 16 // 3, B)))
+        w.free(rng.random(B) < 0.3)
+        w.fork(np.where(rng.random(B) < 0.2, rng.integers(0, B, B), -1))
+        w.same()
+    w.compact()
+    w.same()
+    assert 0 in seen
+
+
 def test_nothing_changes_when_pages_run_out():
     w = Both(4, 8, 12, 16)
     assert w.extend([40, 20, 16, 0]) == 0
