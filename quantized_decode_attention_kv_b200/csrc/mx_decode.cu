@@ -16,15 +16,21 @@
 // The softmax reference of a row moves only when a score passes it by 2^15 (a vote in the warp);
 // the frequent path has no cross-lane reduction.
 //
-// A step takes 32 tokens (two such tiles): with 16 a third more instructions went to copies, waits
-// and votes. Work: the space of 32-token tiles of all (sequence, KV head, row block) units is flattened and
+// Work: the space of 32-token tiles of all (sequence, KV head, row block) units is flattened and
 // divided evenly over all warps of the grid on the device, from the lengths in device memory, so a
 // captured graph follows lengths that change and a ragged batch stays balanced. A unit counts
 // kUnitCost tiles more than it has (queries, page table, output). Each warp copies its own tiles
 // with cp.async into a ring of its own, ahead across units, and waits for no other warp until its
 // stretch is done. Units within a stretch are finished by their warp; the others leave partials in
 // shared memory, joined by the CTA, and those cut by a CTA boundary in the workspace, joined by the
-// combine kernel.
+// combine kernel. (With a CTA's warps sharing each unit, meeting at its end, a ragged batch of 32 took
+// 155 us; this way 25 us. Joining in the CTA that arrives last, in place of the combine kernel, saved
+// 2.4 us on the host and cost up to 9 us on the GPU, where one CTA had two long joins to do.)
+//
+// Bound: HBM by its bytes (144 a token and KV head at D = 128), instructions in practice. 16 x 32K
+// positions of 8 heads, D = 128, 4 query heads each: 604 MB in 119 us (5.1 TB/s, 78% of the copy rate;
+// the copies alone take 99 us), 275 warp instructions for 16 tokens, of which 64 conversions, 64
+// scalings and 17 MMAs. A step takes 32 tokens: with 16 it took 314 instructions and 126 us.
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
@@ -42,21 +48,26 @@ using namespace mma_ops;
 constexpr float kRefDrop = 11.0f;  // the reference sits 2^11 below the largest score seen ...
 constexpr float kRefSlack = 15.0f; // ... and follows when a weight would pass 2^15 (fp16 ends at 2^16)
 constexpr float kRefEmpty = -FLT_MAX;
-constexpr int kUnitCost = 2; // what a unit costs besides its tiles, in tiles
-constexpr int kMinTiles = 2; // tiles a warp gets at least (unit costs included)
+// What a unit costs besides its tiles, in tiles. 1, 2, 4: ragged batch of 32 27.3, 24.9, 24.3 us; 512 units
+// of 20 positions 9.0, 10.3, 12.0 us.
+constexpr int kUnitCost = 2;
+constexpr int kMinTiles = 2; // tiles a warp gets at least, unit costs included (2, 4: 333 positions 9.8, 12.2 us)
 constexpr int kSub = 2;      // 16-token MMA tiles of a tile
 
-// Shapes of the grid: CTAs of an SM, tiles in a warp's ring.
+// Shapes of the grid: CTAs of an SM, tiles in a warp's ring. One column tile of D = 128 needs about 165
+// registers: 12 warps an SM of 168 take 128 us for 16 x 32K positions, 16 warps of 128 spill (146 us).
+// More column tiles keep their queries in shared memory (four queries of 8 x 9001 positions: 57 us with
+// them in registers, 39 us).
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 template <int D, int NT>
 struct Cfg {
   static constexpr int kCtas = D == 64 && NT == 1 ? 4 : D == 256 || NT == 3 || (D == 128 && NT == 2) ? 2 : 3;
-  static constexpr bool kQueriesInSmem = NT > 1;       // the registers hold NT times the sums
-  static constexpr int kStages = D == 64 || (D == 128 && NT < 3) ? 3 : 2;
-  static constexpr int kSixteen = 18 * D;                 // bytes: 16 x (D/2 + D/16) of keys and of values
+  static constexpr bool kQueriesInSmem = NT > 1;
+  static constexpr int kStages = D == 64 || (D == 128 && NT < 3) ? 3 : 2; // what fits
+  static constexpr int kSixteen = 18 * D;            // bytes: 16 x (D/2 + D/16) of keys and of values
   static constexpr int kTile = kSub * kSixteen;
-  static constexpr int kSlot = 8 * NT * (D + 2) * 4;   // bytes of a partial: sums, then (reference, weight sum)
+  static constexpr int kSlot = 8 * NT * (D + 2) * 4; // bytes of a partial: sums, then (reference, weight sum)
   static constexpr int kQueries = kQueriesInSmem ? 16 * D * NT : 0;
   static constexpr int kWarpBytes = kStages * kTile + kSlot + kQueries;
   static constexpr int kSmem = kWarps * kWarpBytes;
@@ -480,6 +491,7 @@ __device__ __forceinline__ void do_tile(uint32_t sm, const Reads<D> &at, const Q
 }
 
 constexpr int kCombineThreads = 256;
+
 // The weighted tile space (below 2^32: the host checks) over the warps of the CTAs that take part:
 // the first `more` shares are one longer than the others.
 struct Split {
@@ -787,57 +799,57 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) mx_decode_kernel(
     do {
       const Cursor cu = s_done[warp];
       const int t0 = cu.first(), t1 = cu.end(len);
-      if (t0 < t1) {
-      const int b = cu.b, h = cu.h, row0 = cu.rb * R;
-      Queries<D, NT> q; // each lane reads what it wrote
-      q.bind(ring_addr + S * C::kTile + lane * 16);
-      float mul[NT][2];
-      int full; // every row of the block sees the positions below
-      {
-        const Rows rows = rows_of(k, b);
-        load_queries<D, NT>(k, rows, b, h, row0, lane, q, mul);
-        const int query = query_of(k, row0);
-        full = query < rows.count ? rows.limit(query) : rows.seen;
-      }
-      Acc<D, NT> acc;
-#pragma unroll
-      for (int n_ = 0; n_ < NT; ++n_) {
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc.o[n_][i][e] = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc.l[n_][e] = 0.0f;
-        acc.ref[n_][0] = acc.ref[n_][1] = kRefEmpty;
-      }
-      for (int tile = t0; tile < t1; ++tile) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
-        __syncwarp(); // all lanes' copies of this tile are there, and the oldest stage's readers are done
-        copy_tile(ring_addr + free_stage);
-        constexpr int kTokens = 16 * kSub;
-        constexpr unsigned kAll = (1u << kSub) - 1u;
-        const unsigned here = mapped >> (kSub * (S - 1)) & kAll;
-        const int pos = tile * kTokens;
-        do_tile<D, NT>(ring_addr + at_stage, reads, q, mul, k, b, row0, pos, here, pos + kTokens > full || here != kAll, lane, acc);
-        free_stage = at_stage;
-        at_stage = at_stage + C::kTile == S * C::kTile ? 0 : at_stage + C::kTile;
-      }
-      if (t0 > 0) {
-        left |= kHead | (t1 == cu.nt ? kHeadEnds : 0);
-        store_partial<D, NT>(reinterpret_cast<float *>(ring + C::kHeadAt), acc, lane);
-      } else if (t1 == cu.nt) {
-        store_whole<D, NT>(k, rows_of(k, b), b, h, row0, acc, lane);
-      } else { // the last unit of the stretch: its partial takes the ring's place
-        left |= kTail;
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        __syncwarp();
-        store_partial<D, NT>(reinterpret_cast<float *>(ring), acc, lane);
-        if (lane == 0) {
-          const uint32_t last = s_bound[warp] + cu.at + cu.nt - 1; // the unit's last tile, in the whole space
-          s_tail[warp] = make_int4(b, h, row0, static_cast<int>(split.share_of(last) / W) - cta + 1);
-          s_rows[warp] = rows_of(k, b);
+      if (t0 < t1) { // else only the cost of a unit lies in the stretch
+        const int b = cu.b, h = cu.h, row0 = cu.rb * R;
+        Queries<D, NT> q; // each lane reads what it wrote
+        q.bind(ring_addr + S * C::kTile + lane * 16);
+        float mul[NT][2];
+        int full; // every row of the block sees the positions below
+        {
+          const Rows rows = rows_of(k, b);
+          load_queries<D, NT>(k, rows, b, h, row0, lane, q, mul);
+          const int query = query_of(k, row0);
+          full = query < rows.count ? rows.limit(query) : rows.seen;
         }
-      }
+        Acc<D, NT> acc;
+#pragma unroll
+        for (int n_ = 0; n_ < NT; ++n_) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc.o[n_][i][e] = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc.l[n_][e] = 0.0f;
+          acc.ref[n_][0] = acc.ref[n_][1] = kRefEmpty;
+        }
+        for (int tile = t0; tile < t1; ++tile) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+          __syncwarp(); // all lanes' copies of this tile are there, and the oldest stage's readers are done
+          copy_tile(ring_addr + free_stage);
+          constexpr int kTokens = 16 * kSub;
+          constexpr unsigned kAll = (1u << kSub) - 1u;
+          const unsigned here = mapped >> (kSub * (S - 1)) & kAll;
+          const int pos = tile * kTokens;
+          do_tile<D, NT>(ring_addr + at_stage, reads, q, mul, k, b, row0, pos, here, pos + kTokens > full || here != kAll, lane, acc);
+          free_stage = at_stage;
+          at_stage = at_stage + C::kTile == S * C::kTile ? 0 : at_stage + C::kTile;
+        }
+        if (t0 > 0) {
+          left |= kHead | (t1 == cu.nt ? kHeadEnds : 0);
+          store_partial<D, NT>(reinterpret_cast<float *>(ring + C::kHeadAt), acc, lane);
+        } else if (t1 == cu.nt) {
+          store_whole<D, NT>(k, rows_of(k, b), b, h, row0, acc, lane);
+        } else { // the last unit of the stretch: its partial takes the ring's place
+          left |= kTail;
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+          __syncwarp();
+          store_partial<D, NT>(reinterpret_cast<float *>(ring), acc, lane);
+          if (lane == 0) {
+            const uint32_t last = s_bound[warp] + cu.at + cu.nt - 1; // the unit's last tile, in the whole space
+            s_tail[warp] = make_int4(b, h, row0, static_cast<int>(split.share_of(last) / W) - cta + 1);
+            s_rows[warp] = rows_of(k, b);
+          }
+        }
       }
       Cursor c = s_done[warp];
       more = c.next(k, len);
