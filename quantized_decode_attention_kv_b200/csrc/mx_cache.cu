@@ -10,7 +10,9 @@
 // between threads. HBM bounds them (write: 2 + 9/16 bytes an element) only while a block takes about
 // 150 instructions, so those are counted: grids without divisions, record numbers of 32 bits, the
 // maximum on packed 16-bit patterns, packed fp32 pairs (16 x 8 x 4096 rows of bf16, 344 MB each way,
-// 53 us at the copy rate: write 98 -> 62 us, read 80 -> 60 us).
+// 53 us at the copy rate: write 98 -> 62 us, read 80 -> 60 us). A read back into padded rows mostly
+// writes zeros, and plain writes reach half the copy rate: 134 MB take 37 us in a fill, and 35 us
+// here with the write of 10 MB before them.
 //
 // Ties are common (16-bit inputs over a 4-bit scale hit an E2M1 midpoint m about once in 64), so
 // x / (S g) has to land on the right side of them; x times r = 1 / (S g) alone does not.
@@ -33,29 +35,27 @@ using namespace mx;
 constexpr int kThreads = 256;
 
 // Which (sequence, head, block) and first row a thread owns. Bulk calls: a CTA takes U times kRows
-// consecutive rows of one head, the grid is (rows, heads of keys and values, sequences), or heads
-// first where the heads of a row lie closer together than the rows of a head (a model's
-// [sequence][row][head] layout), so that neighbours in time are neighbours in memory: zeros for 134 MB
-// of padding took 36 us with heads first, 29 us with rows first. Small calls (one new token):
-// 2^tshift rows of each of some heads, the grid is (heads of all sequences, 1, keys and values).
+// consecutive rows of one head, the grid is (rows, heads of keys and values, sequences). Small calls
+// (one new token): 2^tshift rows of each of some heads, the grid is (heads of all sequences, 1, keys
+// and values).
 struct RowIndex {
   int which, b, h, t, blk;
   bool ok;
 };
 
 template <int D, bool kBulk, int U>
-__device__ __forceinline__ RowIndex row_index(const MxRowsArgs &a, int tshift, bool heads_first) {
+__device__ __forceinline__ RowIndex row_index(const MxRowsArgs &a, int tshift) {
   constexpr int kPer = D / kBlock, kRows = kThreads / kPer;
   const int r = threadIdx.x / kPer;
   RowIndex i;
   i.blk = threadIdx.x % kPer;
   if constexpr (kBulk) {
-    const int head = heads_first ? blockIdx.x : blockIdx.y;
+    const int head = blockIdx.y;
     const bool second = head >= a.c.Hkv;
     i.which = second || !a.x[0];
     i.h = head - (second ? a.c.Hkv : 0);
     i.b = blockIdx.z;
-    i.t = (heads_first ? blockIdx.y : blockIdx.x) * (U * kRows) + r;
+    i.t = blockIdx.x * (U * kRows) + r;
     i.ok = i.t < a.T;
   } else {
     const int bh = static_cast<int>(blockIdx.x) * (kRows >> tshift) + (r >> tshift);
@@ -68,9 +68,10 @@ __device__ __forceinline__ RowIndex row_index(const MxRowsArgs &a, int tshift, b
   return i;
 }
 
+__device__ __forceinline__ uint32_t dup_low(uint32_t h) { return __byte_perm(h, 0u, 0x1010u); } // the low half twice
+
 // Records of the thread's rows: kNone where a row is none of the sequence's, or not on a mapped page.
 // (Codes are at most 64 GiB, so records are below 2^31.) Returns the number of rows of the sequence.
-__device__ __forceinline__ uint32_t dup_low(uint32_t h) { return __byte_perm(h, 0u, 0x1010u); }
 constexpr uint32_t kNone = 0xFFFFFFFFu;
 template <int D, int U>
 __device__ __forceinline__ int find_rows(const MxRowsArgs &a, const RowIndex &i, uint32_t (&rec)[U]) {
@@ -97,10 +98,10 @@ __device__ __forceinline__ int find_rows(const MxRowsArgs &a, const RowIndex &i,
 
 // kPow2: 16-bit inputs and tensor scales that are powers of two.
 template <int D, int DT, bool kBulk, int U, bool kPow2>
-__global__ void __launch_bounds__(kThreads) mx_write_kernel(const MxRowsArgs a, int tshift, bool heads_first) {
+__global__ void __launch_bounds__(kThreads) mx_write_kernel(const MxRowsArgs a, int tshift) {
   constexpr int kRows = kThreads / (D / kBlock), kSize = DT == TQ_F32 ? 4 : 2, kVecs = kBlock * kSize / 16;
   pdl_wait();
-  const RowIndex i = row_index<D, kBulk, U>(a, tshift, heads_first);
+  const RowIndex i = row_index<D, kBulk, U>(a, tshift);
   if (!i.ok) return;
   uint32_t rec[U];
   const int n = find_rows<D, U>(a, i, rec);
@@ -189,10 +190,10 @@ __global__ void __launch_bounds__(kThreads) mx_write_kernel(const MxRowsArgs a, 
 }
 
 template <int D, int DT, bool kBulk, int U>
-__global__ void __launch_bounds__(kThreads) mx_read_kernel(const MxRowsArgs a, int tshift, bool heads_first) {
+__global__ void __launch_bounds__(kThreads) mx_read_kernel(const MxRowsArgs a, int tshift) {
   constexpr int kRows = kThreads / (D / kBlock), kSize = DT == TQ_F32 ? 4 : 2;
   pdl_wait();
-  const RowIndex i = row_index<D, kBulk, U>(a, tshift, heads_first);
+  const RowIndex i = row_index<D, kBulk, U>(a, tshift);
   if (!i.ok) return;
   uint32_t rec[U];
   find_rows<D, U>(a, i, rec);
@@ -254,8 +255,11 @@ __global__ void __launch_bounds__(kThreads) mx_read_kernel(const MxRowsArgs a, i
         even_half[e] = odd ? got : out[k + e];
         odd_half[e] = odd ? out[k + 4 + e] : got;
       }
-      *reinterpret_cast<uint4 *>(to + 4 * k) = make_uint4(even_half[0], even_half[1], even_half[2], even_half[3]);
-      *reinterpret_cast<uint4 *>(to + 4 * k + kBlock * kSize) = make_uint4(odd_half[0], odd_half[1], odd_half[2], odd_half[3]);
+      const uint4 x = make_uint4(even_half[0], even_half[1], even_half[2], even_half[3]);
+      const uint4 y = make_uint4(odd_half[0], odd_half[1], odd_half[2], odd_half[3]);
+      uint4 *first = reinterpret_cast<uint4 *>(to + 4 * k), *second = reinterpret_cast<uint4 *>(to + 4 * k + kBlock * kSize);
+      if constexpr (kBulk) __stcs(first, x), __stcs(second, y); // more than the L2 holds, as a rule: 2 us of 37
+      else *first = x, *second = y;
     }
   }
 }
@@ -270,23 +274,19 @@ cudaError_t run_rows_u(const MxRowsArgs &a, bool write, cudaStream_t s) {
   constexpr int kRows = kThreads / (D / kBlock);
   const unsigned sides = a.x[0] && a.x[1] ? 2 : 1;
   int tshift = 0;
-  bool heads_first = false;
   dim3 grid;
   if (kBulk) {
-    const long long *st = a.st[a.x[0] ? 0 : 1];
-    const unsigned heads = sides * a.c.Hkv, across = (a.T + U * kRows - 1) / (U * kRows);
-    heads_first = st[1] < st[2] && across <= 65535;
-    grid = heads_first ? dim3(heads, across, a.c.B) : dim3(across, heads, a.c.B);
+    grid = dim3((a.T + U * kRows - 1) / (U * kRows), sides * a.c.Hkv, a.c.B);
   } else {
     while ((1 << tshift) < a.T) ++tshift;
     const long long heads = static_cast<long long>(a.c.B) * a.c.Hkv, per = kRows >> tshift;
     grid = dim3(static_cast<unsigned>((heads + per - 1) / per), 1, sides);
   }
-  if (!write) return launch_pdl(mx_read_kernel<D, DT, kBulk, U>, grid, dim3(kThreads), 0, s, a, tshift, heads_first);
+  if (!write) return launch_pdl(mx_read_kernel<D, DT, kBulk, U>, grid, dim3(kThreads), 0, s, a, tshift);
   if constexpr (DT != TQ_F32)
     if ((!a.x[0] || power_of_two(a.c.g[0])) && (!a.x[1] || power_of_two(a.c.g[1])))
-      return launch_pdl(mx_write_kernel<D, DT, kBulk, U, true>, grid, dim3(kThreads), 0, s, a, tshift, heads_first);
-  return launch_pdl(mx_write_kernel<D, DT, kBulk, U, false>, grid, dim3(kThreads), 0, s, a, tshift, heads_first);
+      return launch_pdl(mx_write_kernel<D, DT, kBulk, U, true>, grid, dim3(kThreads), 0, s, a, tshift);
+  return launch_pdl(mx_write_kernel<D, DT, kBulk, U, false>, grid, dim3(kThreads), 0, s, a, tshift);
 }
 
 // Small calls have less than a CTA's rows of a head; bulk calls take four rows a thread where that leaves

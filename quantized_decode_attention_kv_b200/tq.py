@@ -579,16 +579,20 @@ def _mx_pair(K, V, cache: TQMXCache):
     return v
 
 
+_Strides = ctypes.c_int64 * 3
+
+
 def _mx_strides(x, name: str):
     """Pointer and row strides (in elements; None where they are those of a contiguous tensor)."""
     if x is None:
         return None, None
     if x.is_contiguous():
         return x.data_ptr(), None
-    s = x.stride()
-    if s[3] != 1:
+    s0, s1, s2, s3 = x.stride()
+    B, Hkv, T, _ = x.shape
+    if s3 != 1:
         raise TQError(TQ_ERR_INVALID_ARG, f"{name}: the elements of a row must be adjacent")
-    return x.data_ptr(), (ctypes.c_int64 * 3)(*(0 if n == 1 else i for n, i in zip(x.shape, s[:3])))
+    return x.data_ptr(), _Strides(s0 if B > 1 else 0, s1 if Hkv > 1 else 0, s2 if T > 1 else 0)
 
 
 def tq_quantize_kv_mx(K: torch.Tensor | None, V: torch.Tensor | None, cache: TQMXCache, lens: torch.Tensor,
