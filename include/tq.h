@@ -306,7 +306,8 @@ int tq_prefill_attention(const void *q, int dtype, int Hq, int Lq, int t0, float
  *   block_table [B][max_pages] int32: page of each logical page; an entry outside
  *     0..num_pages-1 (-1, say) is an unmapped page: writes to it are dropped, reads give zeros,
  *     attention does not see it.
- * d is 64, 128 or 256; k_scale and v_scale (g) lie in 2^-64..2^64. All lengths and tables are
+ * d is 64, 128 or 256; k_scale and v_scale (g) lie in 2^-64..2^64; the codes of a tensor are at most
+ * 64 GiB, max_pages * page_size at most 2^30. All lengths and tables are
  * read on the device when the kernels run, so captured graphs follow them.
  *
  * Rows of a batch: the calls below take `rows` rows of every sequence (T new tokens, Lq queries),
@@ -345,7 +346,8 @@ int tq_dequantize_mx(const tq_mx_cache *cache, int T, const int32_t *lens, const
  * a query that sees none, and rows of no sequence, give zeros. What a query does not see cannot
  * reach its output, NaN included. Sums and softmax in fp32; keys, values and queries enter the
  * tensor cores exactly (fp16 products of 6- and 11-bit significands), softmax weights in fp16.
- * Lq is 1..16, Hq a multiple of Hkv. The workspace depends on d only (not on the lengths, Hq or
+ * Lq is 1..16, Hq a multiple of Hkv; the 16-position tiles of all sequences at full length, times KV
+ * heads and blocks of 8 rows (Lq Hq / Hkv), must stay below 2^32. The workspace depends on d only (not on the lengths, Hq or
  * Lq): one serves decode steps and drafts in turn; calls that may overlap on the GPU need one each. Errors: TQ_ERR_INVALID_ARG,
  * TQ_ERR_UNSUPPORTED, TQ_ERR_WORKSPACE, TQ_ERR_CUDA. */
 size_t tq_decode_mx_workspace_bytes(int Hq, int Lq, const tq_mx_cache *cache);

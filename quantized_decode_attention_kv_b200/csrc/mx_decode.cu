@@ -62,9 +62,9 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 template <int D, int NT>
 struct Cfg {
-  static constexpr int kCtas = D == 64 && NT == 1 ? 4 : D == 256 || NT == 3 || (D == 128 && NT == 2) ? 2 : 3;
+  static constexpr int kCtas = D == 64 && NT == 1 ? 4 : D == 256 || (D == 128 && NT == 2) ? 2 : 3;
   static constexpr bool kQueriesInSmem = NT > 1;
-  static constexpr int kStages = D == 64 || (D == 128 && NT < 3) ? 3 : 2; // what fits
+  static constexpr int kStages = D == 256 ? 2 : 3; // what fits
   static constexpr int kSixteen = 18 * D;            // bytes: 16 x (D/2 + D/16) of keys and of values
   static constexpr int kTile = kSub * kSixteen;
   static constexpr int kSlot = 8 * NT * (D + 2) * 4; // bytes of a partial: sums, then (reference, weight sum)
@@ -972,8 +972,8 @@ cudaError_t run(const Kernel &k, const MxPlan &p, cudaStream_t s) {
 
 template <class F>
 auto with_shape(int d, int nt, F &&f) { // f.operator()<D, NT>()
-  if (d == 64) return nt == 1 ? f.template operator()<64, 1>() : nt == 2 ? f.template operator()<64, 2>() : f.template operator()<64, 3>();
-  if (d == 128) return nt == 1 ? f.template operator()<128, 1>() : nt == 2 ? f.template operator()<128, 2>() : f.template operator()<128, 3>();
+  if (d == 64) return nt == 1 ? f.template operator()<64, 1>() : f.template operator()<64, 2>();
+  if (d == 128) return nt == 1 ? f.template operator()<128, 1>() : f.template operator()<128, 2>();
   return f.template operator()<256, 1>();
 }
 
@@ -994,11 +994,15 @@ struct Launch {
 MxPlan plan_mx_decode(int Hkv, int d, int Hq, int Lq, int device, int sm_count) {
   MxPlan p;
   p.device = device;
-  const int rows = Lq * (Hq / Hkv), most = d == 256 ? 1 : 3;
-  p.row_blocks = (rows + 8 * most - 1) / (8 * most);
-  p.nt = (rows + 8 * p.row_blocks - 1) / (8 * p.row_blocks);
+  // A block of 16 rows takes about 1.6 times as long as one of 8 (operands are made once for both), so it
+  // is taken where it halves the blocks or nearly so: 16 rows of 8 x 9001 positions 37.8 us against 42.9,
+  // 128 rows of 8 x 4000 93 against 118, but 20 rows, 700..9001 positions, 32.1 against 29.3 in three
+  // blocks of 8. (24 rows a block: 33.9 us there, 94.8 us for 128 rows.) Heads of 256 leave room for one.
+  const int rows = Lq * (Hq / Hkv), of8 = (rows + 7) / 8, of16 = (rows + 15) / 16, most = d == 256 ? 1 : 2;
+  p.nt = most == 2 && 5 * of8 >= 8 * of16 ? 2 : 1;
+  p.row_blocks = p.nt == 2 ? of16 : of8;
   p.ctas = sm_count * with_shape(d, p.nt, Ctas{});
-  // one size serves every number of queries and heads: the largest of the tile counts'
+  // one size serves every number of queries and heads: the larger of the block sizes'
   p.ws_bytes = 0;
   for (int nt = 1; nt <= most; ++nt) {
     const size_t ctas = static_cast<size_t>(sm_count) * with_shape(d, nt, Ctas{});

@@ -343,11 +343,11 @@ def _check(cache, q, lens, counts=None, scale=None, out_dtype=None):
     (64, 2, 5, 3, 128, [250, 3, 129, 64], "bf16", "f32"),      # 15 rows: two column tiles
     (256, 2, 2, 1, 64, [200, 65, 1], "bf16", "bf16"),
     (256, 1, 3, 4, 16, [90, 4, 100], "f16", "f32"),            # 12 rows in two blocks
-    (128, 2, 4, 5, 16, [100, 5, 47, 16], "bf16", "f32"),       # 20 rows in two blocks of 16
-    (128, 1, 8, 16, 32, [64, 16, 200], "f16", "f32"),          # 128 rows in eight blocks
+    (128, 2, 4, 5, 16, [100, 5, 47, 16], "bf16", "f32"),       # 20 rows: three blocks
+    (128, 1, 8, 16, 32, [64, 16, 200], "f16", "f32"),          # 128 rows: eight blocks of 16
     (64, 1, 7, 2, 16, [31, 33], "f16", "bf16"),
-    (64, 2, 6, 4, 32, [120, 33, 4, 64], "bf16", "f32"),        # 24 rows: three column tiles
-    (128, 1, 11, 2, 16, [15, 16, 17, 31, 32, 33, 48, 65], "bf16", "f16"),  # 22 rows, ends within a step of 32
+    (64, 2, 6, 4, 32, [120, 33, 4, 64], "bf16", "f32"),        # 24 rows: three blocks
+    (128, 1, 11, 2, 16, [15, 16, 17, 31, 32, 33, 48, 65], "bf16", "f16"),  # 22 rows; ends within a step of 32
     (64, 3, 2, 1, 64, [15, 16, 17, 31, 32, 33, 48, 63, 65, 96], "f16", "f32"),
     (256, 2, 8, 1, 128, [1000, 31, 130], "f16", "f32"),
     (128, 8, 4, 1, 64, [3000], "bf16", "f32"),                 # few units, many CTAs each
