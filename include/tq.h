@@ -297,7 +297,7 @@ int tq_prefill_attention(const void *q, int dtype, int Hq, int Lq, int t0, float
  * codebook, no per-vector norm). A block x with top = max |x| is stored as
  *   S    = E4M3(min(top / (6 g), 448))        one byte, to nearest, ties to even
  *   code = E2M1(x_i / (S g))                  4 bits, to nearest, ties to even, saturating at 6
- * and stands for E2M1 * S * g. Blocks whose top is below about 2^-10 * 6 g have S = 0 and stand
+ * (quotients in fp32) and stands for E2M1 * S * g. Blocks whose top is below about 2^-10 * 6 g have S = 0 and stand
  * for zeros; a NaN or infinity in a block makes its S NaN (0x7F), so that it stays visible.
  *
  * Per tensor, in pages of page_size positions (a power of two, >= 16):

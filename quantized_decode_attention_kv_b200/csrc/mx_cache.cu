@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kThreads) mx_write_kernel(const MxRowsArgs a, 
             v[k] = f2(f.x, f.y);
           }
         }
-        if (t > 448.0f) { // saturated: larger elements are 6 all the same; keeps the quotients small
+        if (!(t <= 448.0f)) { // saturated (NaN: top / (6 g) passes fp32): larger elements are 6 all the same
 #pragma unroll
           for (int k = 0; k < kBlock / 2; ++k) {
             float x, y;

@@ -250,6 +250,25 @@ def test_write_of_special_values(dtype):
     assert torch.isnan(out[0, 0, 1, :16]).all() and (out[0, 0, 1, 20] > 0)
 
 
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("g", [2.0 ** -64, 1.3 * 2.0 ** -63, 2.0 ** 64])
+def test_values_far_above_and_below_the_scale(dtype, g):
+    # top / (6 g) passes fp32 (saturates: every larger element is 6, signs stay), or is far below 2^-10 (zeros)
+    t = DT[dtype]
+    x = torch.zeros(1, 1, 3, 64)
+    x[0, 0, 0], x[0, 0, 0, ::3] = torch.finfo(t).max, -torch.finfo(t).max
+    x[0, 0, 1, :4] = torch.tensor([1.0, -1e4, 3e4, -torch.finfo(t).max])
+    x[0, 0, 2] = torch.finfo(t).smallest_normal
+    x = x.to(t).cuda()
+    cache = _cache(1, 1, 64, 16, 1, g=(g, g))
+    tq.tq_quantize_kv_mx(x, x, cache, _i32([3]))
+    codes, s = M.quantise(_np(x[0, 0]), np.float32(g), np.float64)
+    for side in "kv":
+        got_c, got_s = _records(cache, side, 0, 0, np.arange(3))
+        np.testing.assert_array_equal(got_s, s)
+        np.testing.assert_array_equal(M.values(got_c, s, 1.0), M.values(M.pack(codes), s, 1.0))
+
+
 def test_write_and_read_leave_out_what_has_no_place():
     B, Hkv, d, page = 5, 2, 64, 16
     cache = _cache(B, Hkv, d, page, 3)
