@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -529,7 +530,7 @@ def _run(fn, device: torch.device, stream, *args) -> None:
         stream = torch._C._cuda_getCurrentRawStream(index)  # a decode step cannot afford building a Stream
     else:
         stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         status = fn(*args, stream)
     else:
         with torch.cuda.device(index):
@@ -553,46 +554,39 @@ def _ws(ws, device: torch.device) -> int:
     return ws.data_ptr()
 
 
-def _mx_rows(x, cache: TQMXCache, name: str):
-    """Checks one [B, Hkv, T, d] tensor; its (dtype, T)."""
-    if isinstance(x, torch.Tensor) and x.device == cache.device and x.dim() == 4:
-        B, Hkv, T, d = x.shape
-        if B == cache.B and Hkv == cache.Hkv and d == cache.d and x.dtype in _DTYPES:
-            return x.dtype, T
-        if x.dtype not in _DTYPES:
-            raise TQError(TQ_ERR_INVALID_ARG, f"{name}: unsupported dtype {x.dtype}")
-    raise TQError(TQ_ERR_INVALID_ARG, f"{name} must be a tensor [B={cache.B}][Hkv={cache.Hkv}][T][d={cache.d}] "
-                  f"on {cache.device}")
+@functools.lru_cache(maxsize=256)
+def _row_strides(shape: tuple, stride: tuple):
+    """Strides of sequences, heads and rows, in elements, of a tensor [B][Hkv][T][d] whose row elements
+    are adjacent; the stride of a dimension of one is of no matter."""
+    if len(shape) != 4 or stride[3] != 1:
+        raise TQError(TQ_ERR_INVALID_ARG, f"K and V must be [B][Hkv][T][d] with adjacent row elements, got shape "
+                      f"{tuple(shape)} and strides {tuple(stride)}")
+    return (ctypes.c_int64 * 3)(*(0 if n == 1 else i for n, i in zip(shape[:3], stride)))
 
 
-def _mx_pair(K, V, cache: TQMXCache):
-    """(dtype, T) of K and V, either of which may be None."""
-    if K is None and V is None:
-        raise TQError(TQ_ERR_INVALID_ARG, "K and V are both None")
-    k = v = None
-    if K is not None:
-        k = v = _mx_rows(K, cache, "K")
-    if V is not None:
-        v = _mx_rows(V, cache, "V")
-    if k is not None and k != v:
-        raise TQError(TQ_ERR_INVALID_ARG, "K and V must share their dtype and T")
-    return v
-
-
-_Strides = ctypes.c_int64 * 3
-
-
-def _mx_strides(x, name: str):
-    """Pointer and row strides (in elements; None where they are those of a contiguous tensor)."""
-    if x is None:
-        return None, None
-    if x.is_contiguous():
-        return x.data_ptr(), None
-    s0, s1, s2, s3 = x.stride()
-    B, Hkv, T, _ = x.shape
-    if s3 != 1:
-        raise TQError(TQ_ERR_INVALID_ARG, f"{name}: the elements of a row must be adjacent")
-    return x.data_ptr(), _Strides(s0 if B > 1 else 0, s1 if Hkv > 1 else 0, s2 if T > 1 else 0)
+def _mx_rows(K, V, cache: TQMXCache, contiguous: bool):
+    """Checks K and V (either may be None): (dtype, T, then pointer and strides of each)."""
+    ref = K if K is not None else V
+    if not isinstance(ref, torch.Tensor):
+        raise TQError(TQ_ERR_INVALID_ARG, "K and V must be tensors, one of them at least")
+    shape, dtype = ref.shape, ref.dtype
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        raise TQError(TQ_ERR_INVALID_ARG, f"unsupported dtype {dtype}")
+    found = []
+    for x in (K, V):
+        if x is None:
+            found += None, None
+            continue
+        if not isinstance(x, torch.Tensor) or x.device != cache.device or x.dtype is not dtype or x.shape != shape:
+            raise TQError(TQ_ERR_INVALID_ARG, f"K and V must be tensors of one shape and dtype on {cache.device}")
+        if contiguous and not x.is_contiguous():
+            raise TQError(TQ_ERR_INVALID_ARG, "K and V must be contiguous")
+        found += x.data_ptr(), None if contiguous else _row_strides(shape, x.stride())
+    if len(shape) != 4 or shape[0] != cache.B or shape[1] != cache.Hkv or shape[3] != cache.d:
+        raise TQError(TQ_ERR_INVALID_ARG, f"K and V must be [B={cache.B}][Hkv={cache.Hkv}][T][d={cache.d}], got "
+                      f"{list(shape)}")
+    return dt, shape[2], *found
 
 
 def tq_quantize_kv_mx(K: torch.Tensor | None, V: torch.Tensor | None, cache: TQMXCache, lens: torch.Tensor,
@@ -600,25 +594,19 @@ def tq_quantize_kv_mx(K: torch.Tensor | None, V: torch.Tensor | None, cache: TQM
     """Write rows of K, V [B, Hkv, T, d] (any strides whose rows are adjacent and 16-byte aligned): row
     t < counts[b] (default: T) is position lens[b] - counts[b] + t of sequence b; lens holds the
     lengths after the write. lens, counts: int32 [B] on the device."""
-    dtype, T = _mx_pair(K, V, cache)
-    kp, ks = _mx_strides(K, "K")
-    vp, vs = _mx_strides(V, "V")
+    dt, T, kp, ks, vp, vs = _mx_rows(K, V, cache, False)
     dev = cache.device
-    _run(lib.tq_quantize_kv_mx, dev, stream, kp, vp, _DTYPES[dtype], T, ks, vs, _i32(lens, cache.B, "lens", dev),
+    _run(lib.tq_quantize_kv_mx, dev, stream, kp, vp, dt, T, ks, vs, _i32(lens, cache.B, "lens", dev),
          None if counts is None else _i32(counts, cache.B, "counts", dev), cache.ref)
 
 
 def tq_dequantize_mx(cache: TQMXCache, lens: torch.Tensor, K: torch.Tensor | None, V: torch.Tensor | None,
                      counts: torch.Tensor | None = None, stream=None) -> None:
     """Read the same rows back into K, V (contiguous [B, Hkv, T, d]); rows that hold none are zeros."""
-    dtype, T = _mx_pair(K, V, cache)
+    dt, T, kp, _, vp, _ = _mx_rows(K, V, cache, True)
     dev = cache.device
-    for x in (K, V):
-        if x is not None and not x.is_contiguous():
-            raise TQError(TQ_ERR_INVALID_ARG, "K and V must be contiguous")
     _run(lib.tq_dequantize_mx, dev, stream, cache.ref, T, _i32(lens, cache.B, "lens", dev),
-         None if counts is None else _i32(counts, cache.B, "counts", dev), None if K is None else K.data_ptr(),
-         None if V is None else V.data_ptr(), _DTYPES[dtype])
+         None if counts is None else _i32(counts, cache.B, "counts", dev), kp, vp, dt)
 
 
 def tq_decode_mx_workspace_bytes(cache: TQMXCache, Hq: int, Lq: int = 1) -> int:
