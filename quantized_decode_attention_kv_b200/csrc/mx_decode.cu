@@ -227,14 +227,15 @@ __device__ __forceinline__ void read_values(uint32_t sm, const Reads<D> &at, Til
 }
 
 // A warp's way through its stretch of the weighted tile space: units one after the other. Positions
-// are relative to the stretch's begin.
+// are relative to the stretch's begin. (Lengths that another stream changes while the kernel runs make
+// wrong outputs, never indexes out of range: sequences and heads are bounded here, CTAs at the joins.)
 struct Cursor {
   int b, nt, h, rb; // sequence, its tiles, KV head, row block
   int at;           // position of the unit's first tile
   __device__ __forceinline__ void start(const Kernel &k, int b0, uint32_t ahead) { // ahead: begin less b0's begin
     b = b0;
     nt = tiles_of(k, b);
-    const uint32_t unit = ahead / (nt + kUnitCost);
+    const uint32_t unit = min(ahead / (nt + kUnitCost), static_cast<uint32_t>(k.c.Hkv * k.row_blocks - 1));
     at = static_cast<int>(unit * (nt + kUnitCost) - ahead) + kUnitCost;
     h = unit / k.row_blocks;
     rb = unit - h * k.row_blocks;
@@ -253,8 +254,10 @@ struct Cursor {
     rb = 0;
     if (++h < k.c.Hkv) return true;
     h = 0;
-    do nt = tiles_of(k, ++b); // ends: the space below the stretch's end lies in some sequence
-    while (nt == 0);
+    do {
+      if (++b >= k.c.B) return false;
+      nt = tiles_of(k, b);
+    } while (nt == 0);
     return true;
   }
 };
@@ -667,6 +670,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) mx_decode_kernel(
   const int cta = blockIdx.x;
   const Split split(total, gridDim.x, W);
   if (tid <= W) s_bound[tid] = split.begin(cta * W + tid);
+  if (tid < W) s_b0[tid] = 0, s_ahead[tid] = 0;
   __syncthreads();
   uint32_t at = before + incl - mine;
   for (int i = 0; i < per; ++i) {
@@ -846,7 +850,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) mx_decode_kernel(
           store_partial<D, NT>(reinterpret_cast<float *>(ring), acc, lane);
           if (lane == 0) {
             const uint32_t last = s_bound[warp] + cu.at + cu.nt - 1; // the unit's last tile, in the whole space
-            s_tail[warp] = make_int4(b, h, row0, static_cast<int>(split.share_of(last) / W) - cta + 1);
+            const int parts = static_cast<int>(min(split.share_of(last) / W, gridDim.x - 1u)) - cta + 1;
+          s_tail[warp] = make_int4(b, h, row0, max(parts, 1));
             s_rows[warp] = rows_of(k, b);
           }
         }

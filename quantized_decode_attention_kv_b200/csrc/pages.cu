@@ -258,10 +258,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
           const int mid = (b0 + b1) >> 1;
           (s_pre[mid] <= k ? b0 : b1) = mid;
         }
-        if constexpr (MODE == kExtend)
-          a.p.block_table[static_cast<long long>(b0) * a.p.max_pages + s_had[b0] + (k - s_pre[b0])] = page;
-        else
+        if constexpr (MODE == kExtend) {
+          const unsigned j = s_had[b0] + (k - s_pre[b0]); // within the row, unless lens changed meanwhile
+          if (j < static_cast<unsigned>(a.p.max_pages)) a.p.block_table[static_cast<long long>(b0) * a.p.max_pages + j] = page;
+        } else {
           ForkWs(a.ws, B).fresh[b0] = page;
+        }
         a.p.refs[page] = 1;
       }
     }
