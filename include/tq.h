@@ -344,7 +344,8 @@ int tq_dequantize_mx(const tq_mx_cache *cache, int T, const int32_t *lens, const
  * or TQ_F16), out [B][Lq][Hq][d] of `out_dtype` (any of the three types). Query i of sequence b
  * stands at position lens[b] - n_b + i and sees the mapped cache positions up to its own;
  * a query that sees none, and rows of no sequence, give zeros. What a query does not see cannot
- * reach its output, NaN included. Sums and softmax in fp32; keys, values and queries enter the
+ * reach its output, NaN included. Where an infinity in a query makes all the scores it sees infinite, the
+ * output is NaN, as their softmax is, for either sign. Sums and softmax in fp32; keys, values and queries enter the
  * tensor cores exactly (fp16 products of 6- and 11-bit significands), softmax weights in fp16.
  * Lq is 1..16, Hq a multiple of Hkv; the 16-position tiles of all sequences at full length, times KV
  * heads and blocks of 8 rows (Lq Hq / Hkv), must stay below 2^32. The workspace depends on d only (not on the lengths, Hq or

@@ -34,6 +34,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
+#include <climits>
 #include <type_traits>
 
 #include "mma_ops.cuh"
@@ -48,6 +49,10 @@ using namespace mma_ops;
 constexpr float kRefDrop = 11.0f;  // the reference sits 2^11 below the largest score seen ...
 constexpr float kRefSlack = 15.0f; // ... and follows when a weight would pass 2^15 (fp16 ends at 2^16)
 constexpr float kRefEmpty = -FLT_MAX;
+// Weight sum of a row that has seen mapped positions, all with scores of -infinity: its softmax is NaN, where
+// a row that has seen none (sum 0) gives zeros. It vanishes beside any weight of a finite score (the largest
+// is 1 or more) and stays below kLostBelow in joins of any number of stretches.
+constexpr float kLost = 0x1p-100f, kLostBelow = 0x1p-60f;
 // What a unit costs besides its tiles, in tiles. 1, 2, 4: ragged batch of 32 27.3, 24.9, 24.3 us; 512 units
 // of 20 positions 9.0, 10.3, 12.0 us.
 constexpr int kUnitCost = 2;
@@ -517,6 +522,37 @@ struct Split {
 
 enum { kHead = 1, kHeadEnds = 2, kTail = 4, kSome = 8 }; // what a warp's stretch left behind
 
+// Rows without a weight that see a mapped position of the stretch [begin, end) get kLost as their sum.
+template <int D, int NT>
+__device__ __forceinline__ void mark_lost(const Kernel &k, const Rows &rows, int b, int row0, int begin, int end,
+                                          int lane, Acc<D, NT> &acc) {
+  bool none = false;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) none |= acc.l[n][0] == 0.0f || acc.l[n][1] == 0.0f;
+  if (!__any_sync(0xffffffffu, none)) return;
+  const int *entries = k.c.bt + static_cast<long long>(b) * k.c.maxp;
+  const int pages = end > begin ? ((end - 1) >> k.c.pshift) + 1 : 0;
+  int first = INT_MAX; // the first mapped position
+#pragma unroll 1
+  for (int j = begin >> k.c.pshift; j < pages; j += 32) {
+    const int page = j + lane < pages ? __ldg(entries + j + lane) : -1;
+    const unsigned hit = __ballot_sync(0xffffffffu, static_cast<unsigned>(page) < static_cast<unsigned>(k.c.num_pages));
+    if (hit) {
+      first = max((j + __ffs(hit) - 1) << k.c.pshift, begin);
+      break;
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      if (acc.l[n][c] == 0.0f && first < rows.limit(query_of(k, row0 + 8 * n + 2 * (lane & 3) + c))) acc.l[n][c] = kLost;
+}
+
+__device__ __forceinline__ float inverse_sum(const Kernel &k, float l) { // times the value scale; off by 2 units in the last place
+  return l < kLostBelow ? __int_as_float(0x7FC00000) : __fdividef(k.c.g[1], l);
+}
+
 // Writes a warp's state as a partial.
 template <int D, int NT>
 __device__ __forceinline__ void store_partial(float *slot, const Acc<D, NT> &acc, int lane) {
@@ -540,13 +576,12 @@ __device__ __forceinline__ long long out_row(const Kernel &k, int b, int h, int 
   return (static_cast<long long>(b) * k.Lq + query) * k.Hq + h * k.G + row - query * k.G;
 }
 
-// Writes four elements of an output row from its sums. The largest weight is 2^11 or more: a sum of 0
-// means that every position was unmapped.
+// Writes four elements of an output row from its sums. A sum of 0 means that every position was unmapped.
 template <int D>
 __device__ __forceinline__ void store_row(const Kernel &k, const Rows &rows, int b, int h, int row, int d, float l,
                                           const float4 &o) {
   const bool some = rows.limit(query_of(k, row)) > 0 && l != 0.0f;
-  const float inv = __fdividef(k.c.g[1], l); // off by 2 units in the last place
+  const float inv = inverse_sum(k, l);
   const long long at = out_row(k, b, h, row) * D + d;
   store_out(k, at, some ? o.x * inv : 0.0f, some ? o.y * inv : 0.0f);
   store_out(k, at + 2, some ? o.z * inv : 0.0f, some ? o.w * inv : 0.0f);
@@ -564,7 +599,7 @@ __device__ __forceinline__ void store_whole(const Kernel &k, const Rows &rows, i
       const int row = row0 + 8 * n + 2 * tig + c;
       if (row >= k.Lq * k.G) continue;
       const bool some = rows.limit(query_of(k, row)) > 0 && acc.l[n][c] != 0.0f; // as in store_row
-      const float inv = some ? __fdividef(k.c.g[1], acc.l[n][c]) : 0.0f;
+      const float inv = some ? inverse_sum(k, acc.l[n][c]) : 0.0f;
       const size_t at = static_cast<size_t>(out_row(k, b, h, row) * D + g * (D / 8));
       float x[D / 8];
 #pragma unroll
@@ -837,6 +872,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) mx_decode_kernel(
           do_tile<D, NT>(ring_addr + at_stage, reads, q, mul, k, b, row0, pos, here, pos + kTokens > full || here != kAll, lane, acc);
           free_stage = at_stage;
           at_stage = at_stage + C::kTile == S * C::kTile ? 0 : at_stage + C::kTile;
+        }
+        {
+          constexpr int kTokens = 16 * kSub;
+          const Rows rows = rows_of(k, b);
+          mark_lost<D, NT>(k, rows, b, row0, t0 * kTokens, min(t1 * kTokens, rows.seen), lane, acc);
         }
         if (t0 > 0) {
           left |= kHead | (t1 == cu.nt ? kHeadEnds : 0);

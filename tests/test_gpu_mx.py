@@ -492,6 +492,57 @@ def test_a_bad_query_row_stays_alone(bad):
     assert torch.isnan(got[0, 1, 3]).all() and int(torch.isnan(got).any(-1).sum()) == 1
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("d,out_dtype", [(64, "f32"), (128, "bf16"), (256, "f16")])
+def test_scores_that_are_all_minus_infinity_give_nan(d, out_dtype, dtype):
+    # keys of one sign in a channel, infinite queries there: every visible score is the same infinity, and
+    # the softmax of such a row is NaN for either sign. 1 and 20 positions: one warp; 100: one CTA; 3000:
+    # several CTAs, joined by the combine kernel.
+    lens, Lq, G = [1, 20, 100, 3000], 3, 4
+    cache = _cache(4, 1, d, 16, 188, seed=27)
+    K = _randn((4, 1, 3008, d), torch.float32, 28, loud=False)
+    K[..., 0] = 4.0  # no code of it is 0
+    tq.tq_quantize_kv_mx(K.cuda(), K.cuda(), cache, _i32([3008] * 4))
+    q = _randn((4, Lq, G, d), DT[dtype], 29, loud=False).cuda()
+    q[:, :, 1, 0], q[:, :, 2, 0] = float("-inf"), float("inf")
+    bt = cache.block_table
+    clean = _attend(cache, q, lens, out_dtype=DT[out_dtype])
+    got = _np(clean)
+    for b, L in enumerate(lens):
+        for i in range(Lq):
+            sees = L - Lq + i >= 0
+            assert np.isnan(got[b, i, 1:3]).all() if sees else (got[b, i] == 0).all()
+            assert np.isfinite(got[b, i, [0, 3]]).all()
+    # unmapped pages first: the queries that see no mapped position stay zeros
+    bt[1, 0] = bt[2, 0] = -1
+    bt[3, :150] = cache.num_pages
+    out = _np(_attend(cache, q, [1, 18, 18, 2402], out_dtype=DT[out_dtype]))
+    for b in (1, 2, 3):
+        assert (out[b, 0] == 0).all() and np.isnan(out[b, 1:, 1:3]).all() and np.isfinite(out[b, 1:][:, [0, 3]]).all()
+    bt[3] = -1  # and nothing mapped at all
+    assert (_np(_attend(cache, q, [1, 18, 18, 2402], out_dtype=DT[out_dtype]))[3] == 0).all()
+
+
+@pytest.mark.parametrize("split", [10, 100, 1500])
+def test_scores_of_minus_infinity_have_no_weight_beside_finite_ones(split):
+    # scale * score passes fp32 below zero for the first positions, whole tiles and stretches of warps
+    # among them, and is 0 for the others
+    T = 2 * split
+    cache = _cache(1, 1, 128, 16, -(-T // 16), seed=31)
+    K = torch.zeros(1, 1, T, 128)
+    K[0, 0, :split, 0] = 6.0
+    V = _randn((1, 1, T, 128), torch.float32, 32, loud=False)
+    tq.tq_quantize_kv_mx(K.cuda(), V.cuda(), cache, _i32([T]))
+    q = torch.zeros(1, 1, 2, 128, dtype=torch.float16, device="cuda")
+    q[0, 0, 0, 0] = -1.0
+    got = _np(_attend(cache, q, [T], scale=1e38, out_dtype=torch.float32))
+    v = _dense(cache)[1][0, 0, :T]
+    for row, see in ((0, v[split:]), (1, v)):
+        # equal weights: exact in fp16, so what rounds is T sums and the merges (2^-23 each) and the division
+        tol = np.abs(see).mean(0) * (T + 64) * 2.0 ** -23 * 2 + np.abs(see.mean(0)) * 2.0 ** -21
+        assert (np.abs(got[0, 0, row] - see.mean(0)) <= tol).all()
+
+
 # ------------------------------------------------------------------ how it is called
 def test_attention_repeats_bit_for_bit_and_shares_a_workspace_in_turn():
     cache = _setup(4, 4, 128, 32, [3000, 1, 700, 64], seed=30)
