@@ -3,6 +3,7 @@
 // the high half.
 #pragma once
 
+#include "mx_walk.cuh"
 #include "tq_device.cuh"
 
 namespace tq {
@@ -57,10 +58,6 @@ __device__ __forceinline__ uint32_t float_to_e2m1(const float *v) {
       : "=r"(r)
       : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return r;
-}
-
-__device__ __forceinline__ int clamp_count(const int *counts, int b, int rows) {
-  return counts ? min(max(__ldg(counts + b), 0), rows) : rows;
 }
 
 } // namespace mx

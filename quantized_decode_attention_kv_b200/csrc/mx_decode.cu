@@ -53,12 +53,6 @@ constexpr float kRefEmpty = -FLT_MAX;
 // a row that has seen none (sum 0) gives zeros. It vanishes beside any weight of a finite score (the largest
 // is 1 or more) and stays below kLostBelow in joins of any number of stretches.
 constexpr float kLost = 0x1p-100f, kLostBelow = 0x1p-60f;
-// What a unit costs besides its tiles, in tiles. 1, 2, 4: ragged batch of 32 27.3, 24.9, 24.3 us; 512 units
-// of 20 positions 9.0, 10.3, 12.0 us.
-constexpr int kUnitCost = 2;
-constexpr int kMinTiles = 2; // tiles a warp gets at least, unit costs included (2, 4: 333 positions 9.8, 12.2 us)
-constexpr int kSub = 2;      // 16-token MMA tiles of a tile
-
 // Shapes of the grid: CTAs of an SM, tiles in a warp's ring. One column tile of D = 128 needs about 165
 // registers: 12 warps an SM of 168 take 128 us for 16 x 32K positions, 16 warps of 128 spill (146 us).
 // More column tiles keep their queries in shared memory (four queries of 8 x 9001 positions: 57 us with
@@ -108,11 +102,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-__device__ __forceinline__ int tiles_of(const Kernel &k, int b) {
-  if (clamp_count(k.counts, b, k.Lq) == 0) return 0;
-  const int cap = k.c.maxp << k.c.pshift;
-  return (min(max(__ldg(k.lens + b), 0), cap) + 16 * kSub - 1) / (16 * kSub);
-}
 // Row r of a unit is query r / G, head r % G of the group. The quotient is at most 40 and G below
 // 2^16, so the float product is off by less than the half step that separates it from a whole number.
 __device__ __forceinline__ int query_of(const Kernel &k, int row) {
@@ -127,23 +116,6 @@ __device__ __forceinline__ void store_out(const Kernel &k, long long i, float a,
   } else {
     *reinterpret_cast<__half2 *>(static_cast<__half *>(k.out) + i) = __floats2half2_rn(a, b);
   }
-}
-
-// Position limits of a row of a unit: row r is query r / G, head r % G of the group; it sees
-// positions below limit(r) (0: none).
-struct Rows {
-  int count, first, seen; // queries of the sequence, position of query 0, cached positions
-  __device__ __forceinline__ int limit(int query) const {
-    return query < count ? min(max(first + query + 1, 0), seen) : 0;
-  }
-};
-__device__ __forceinline__ Rows rows_of(const Kernel &k, int b) {
-  Rows r;
-  const int len = __ldg(k.lens + b), cap = k.c.maxp << k.c.pshift;
-  r.count = clamp_count(k.counts, b, k.Lq);
-  r.first = len - r.count;
-  r.seen = min(max(len, 0), cap);
-  return r;
 }
 
 // Codes and scale bytes of one 16-token tile, as a lane holds them: rows g and g + 8 of the keys
@@ -230,42 +202,6 @@ __device__ __forceinline__ void read_values(uint32_t sm, const Reads<D> &at, Til
     t.vs[s] = lds_bytes<(D == 256 ? 2 : 1)>(sm + at.vs + ((s >> 1) * 8 + (s & 1)) * (D / 16));
   }
 }
-
-// A warp's way through its stretch of the weighted tile space: units one after the other. Positions
-// are relative to the stretch's begin. (Lengths that another stream changes while the kernel runs make
-// wrong outputs, never indexes out of range: sequences and heads are bounded here, CTAs at the joins.)
-struct Cursor {
-  int b, nt, h, rb; // sequence, its tiles, KV head, row block
-  int at;           // position of the unit's first tile
-  __device__ __forceinline__ void start(const Kernel &k, int b0, uint32_t ahead) { // ahead: begin less b0's begin
-    b = b0;
-    nt = tiles_of(k, b);
-    const uint32_t unit = min(ahead / (nt + kUnitCost), static_cast<uint32_t>(k.c.Hkv * k.row_blocks - 1));
-    at = static_cast<int>(unit * (nt + kUnitCost) - ahead) + kUnitCost;
-    h = unit / k.row_blocks;
-    rb = unit - h * k.row_blocks;
-  }
-  __device__ __forceinline__ int first() const { return max(-at, 0); }
-  __device__ __forceinline__ int end(int len) const { return min(max(len - at, 0), nt); }
-  // 16-token tiles from the unit's begin to its end within the stretch
-  __device__ __forceinline__ int end16(const Kernel &k, int len) const {
-    return min(kSub * end(len), (rows_of(k, b).seen + 15) >> 4);
-  }
-  // the next unit that begins within the stretch; false at its end
-  __device__ __forceinline__ bool next(const Kernel &k, int len) {
-    at += nt + kUnitCost;
-    if (at - kUnitCost >= len) return false;
-    if (++rb < k.row_blocks) return true;
-    rb = 0;
-    if (++h < k.c.Hkv) return true;
-    h = 0;
-    do {
-      if (++b >= k.c.B) return false;
-      nt = tiles_of(k, b);
-    } while (nt == 0);
-    return true;
-  }
-};
 
 // One warp's running state over its tiles.
 template <int D, int NT>
@@ -499,26 +435,6 @@ __device__ __forceinline__ void do_tile(uint32_t sm, const Reads<D> &at, const Q
 }
 
 constexpr int kCombineThreads = 256;
-
-// The weighted tile space (below 2^32: the host checks) over the warps of the CTAs that take part:
-// the first `more` shares are one longer than the others.
-struct Split {
-  uint32_t total, each, more;
-  __device__ __forceinline__ Split(uint32_t n, int ctas, int warps) {
-    total = n;
-    const uint32_t shares = min(static_cast<uint32_t>(ctas), max(n / (warps * kMinTiles), 1u)) * warps;
-    each = n / shares;
-    more = n - each * shares;
-  }
-  __device__ __forceinline__ uint32_t begin(uint32_t i) const { // shares behind the last one begin at the end
-    const uint64_t at = static_cast<uint64_t>(i) * each + min(i, more);
-    return at < total ? static_cast<uint32_t>(at) : total;
-  }
-  __device__ __forceinline__ uint32_t share_of(uint32_t at) const {
-    const uint32_t bend = more * (each + 1);
-    return at < bend ? at / (each + 1) : more + (at - bend) / each;
-  }
-};
 
 enum { kHead = 1, kHeadEnds = 2, kTail = 4, kSome = 8 }; // what a warp's stretch left behind
 
