@@ -391,7 +391,11 @@ int tq_mx_cache_arrays(const tq_mx_cache *cache, tq_page_array *out);
 size_t tq_pages_workspace_bytes(const tq_page_pool *pool);
 
 /* Add max(need[b], 0) positions to every sequence (need: device int32 [B]): lens[b] grows by it and
- * the pages it takes are the lowest-numbered free ones, in the order of (b, logical page). */
+ * the pages it takes are the lowest-numbered free ones, in the order of (b, logical page). Pages that
+ * a sequence still holds behind its length, because the caller lowered lens[b] after rejected
+ * drafts, go back first (whatever the status, and where need[b] is 0 too), and are free for the same call.
+ * A length may be lowered to where the sequence last forked or was forked, at most: the page that it
+ * then ends in is its own. (To go back further, fork it at the lower length into an empty row.) */
 int tq_pages_extend(const tq_page_pool *pool, const int32_t *need, int32_t *status, void *stream);
 
 /* Sequence b becomes a copy of sequence parent_of[b] (device int32 [B]; values outside 0..B-1, and

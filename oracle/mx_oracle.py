@@ -110,6 +110,11 @@ class Pages:
         return -(-int(length) // self.ps)
 
     def extend(self, need):
+        for b, n in enumerate(self.lens):  # pages behind a length that the caller lowered go back first
+            for j in range(self._n(max(int(n), 0)), self.max_pages):
+                if 0 <= self.table[b, j] < len(self.refs):
+                    self.refs[self.table[b, j]] -= 1
+                    self.table[b, j] = -1
         after = [int(n) + max(int(x), 0) for n, x in zip(self.lens, need)]
         if any(a > self.max_pages * self.ps for a in after):
             return 2

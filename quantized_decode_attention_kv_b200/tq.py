@@ -703,7 +703,8 @@ def _pool_arrays(pool: TQPagePool, arrays: TQPageArrays | None):
 
 def tq_pages_extend(pool: TQPagePool, need: torch.Tensor, status: torch.Tensor, stream=None) -> None:
     """lens[b] += need[b] (int32 [B]), with the lowest free pages. status (int32, one element): 0, or
-    1 (not enough free pages) or 2 (a sequence would pass max_pages) and nothing changed."""
+    1 (not enough free pages) or 2 (a sequence would pass max_pages) and nothing changed. Pages behind a
+    length that the caller lowered (rejected drafts) go back first, in any case."""
     _run(lib.tq_pages_extend, pool.device, stream, pool.ref, _i32(need, pool.B, "need", pool.device),
          _i32(status, -1, "status", pool.device))
 

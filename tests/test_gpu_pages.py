@@ -151,6 +151,50 @@ def test_pages_held_by_the_caller_stay_allocated():
     w.same()
 
 
+@pytest.mark.parametrize("B,max_pages,num_pages,page", [
+    (1, 4, 4, 16), (3, 6, 14, 16), (40, 9, 131, 32), (1500, 3, 5000, 16), (5, 200, 600, 64),
+    (24, 900, 40_000, 16), (300, 900, 400_003, 16),  # planned by several blocks, the last beyond their bit masks
+])
+def test_pages_behind_a_lowered_length_go_back(B, max_pages, num_pages, page):
+    """Drafts are written, some are rejected (the caller lowers lens), the next step extends: no page is
+    lost, and pages that others share with the one that stepped back stay theirs."""
+    rng = np.random.default_rng(B + num_pages)
+    w = Both(B, max_pages, num_pages, page, layers=0)
+    seen = set()
+    for step in range(8 if num_pages < 10_000 else 3):
+        seen.add(w.extend(np.where(rng.random(B) < 0.6, rng.integers(0, max_pages * page // 2 + 1, B), 0)))
+        if step % 2 == 1:
+            w.fork(np.where(rng.random(B) < 0.2, rng.integers(0, B, B), -1))
+        low = np.where(rng.random(B) < 0.5, w.want.lens - rng.integers(0, 4 * page, B), w.want.lens).clip(0)
+        w.want.lens[:] = low
+        w.pool.lens.copy_(_i32(low))
+        seen.add(w.extend(np.where(rng.random(B) < 0.5, rng.integers(0, page + 1, B), 0)))
+        w.same()
+        held = w.want.table[w.want.table >= 0]
+        assert np.array_equal(np.bincount(held, minlength=num_pages), w.want.refs)
+    assert 0 in seen
+    w.free([1] * B)
+    w.same()
+    assert int(w.pool.refs.sum()) == 0
+
+
+def test_a_page_that_goes_back_serves_the_same_call():
+    w = Both(2, 4, 4, 16)
+    assert w.extend([33, 16]) == 0  # all four pages
+    for lens in (w.pool.lens, w.want.lens):
+        lens[0] = 16
+    assert w.extend([1, 1]) == 0 and int((w.pool.refs == 0).sum()) == 0
+    w.same()
+    for lens in (w.pool.lens, w.want.lens):
+        lens[0] = 0
+    assert w.extend([0, 0]) == 0 and int((w.pool.refs == 0).sum()) == 2  # no need: the pages go back all the same
+    w.same()
+    for lens in (w.pool.lens, w.want.lens):
+        lens[1] = 3
+    assert w.extend([0, 100]) == 2 and w.extend([64, 0]) == 1
+    w.same()
+
+
 @pytest.mark.parametrize("n", [1, 5, 700])  # 700: more pairs than one launch carries
 def test_copy_moves_listed_pages_only(n):
     w = Both(1, 4, 1500, 16, layers=2, d=128, Hkv=3)
