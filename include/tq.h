@@ -398,6 +398,14 @@ size_t tq_pages_workspace_bytes(const tq_page_pool *pool);
  * then ends in is its own. (To go back further, fork it at the lower length into an empty row.) */
 int tq_pages_extend(const tq_page_pool *pool, const int32_t *need, int32_t *status, void *stream);
 
+/* The same, and granted[b] (device int32 [B], need itself allowed) gets the positions added: max(need[b], 0),
+ * or 0 for every sequence when status is not 0. Give `granted` as counts to the write and the
+ * attention of a step that cannot wait for the status on the host: when there was no room they
+ * write nothing and give zeros. With `need` as counts they would take the LAST need[b] positions of the
+ * unchanged sequences for the new ones, and write over them and over pages that forks share. */
+int tq_pages_extend_granted(const tq_page_pool *pool, const int32_t *need, int32_t *granted, int32_t *status,
+                            void *stream);
+
 /* Sequence b becomes a copy of sequence parent_of[b] (device int32 [B]; values outside 0..B-1, and
  * b itself: b stays as it is). All parents are read as they were, so rows may swap. The child's
  * old pages are given back; it shares the parent's full pages (refs + 1) and gets its own copy of

@@ -268,7 +268,17 @@ int tq_pages_extend(const tq_page_pool *pool, const int32_t *need, int32_t *stat
   if (st) return st;
   if (!aligned(need, 4) || !aligned(status, 4))
     return fail(TQ_ERR_INVALID_ARG, "need/status must be non-NULL and 4-byte aligned");
-  return cuda_status(tq::launch_pages_extend(*pool, need, status, static_cast<cudaStream_t>(stream)),
+  return cuda_status(tq::launch_pages_extend(*pool, need, nullptr, status, static_cast<cudaStream_t>(stream)),
+                     "page extend launch");
+}
+
+int tq_pages_extend_granted(const tq_page_pool *pool, const int32_t *need, int32_t *granted, int32_t *status,
+                            void *stream) {
+  int st = check_pool(pool);
+  if (st) return st;
+  if (!aligned(need, 4) || !aligned(granted, 4) || !aligned(status, 4))
+    return fail(TQ_ERR_INVALID_ARG, "need/granted/status must be non-NULL and 4-byte aligned");
+  return cuda_status(tq::launch_pages_extend(*pool, need, granted, status, static_cast<cudaStream_t>(stream)),
                      "page extend launch");
 }
 

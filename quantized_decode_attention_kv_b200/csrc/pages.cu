@@ -61,6 +61,7 @@ struct PlanArgs {
   int shift;     // log2(page size)
   const int *in; // extend: positions to add; fork: parents
   int *status;   // extend, fork
+  int *granted;  // extend: positions added, or NULL; may be `in`
   int *live;     // compact
   void *ws;
   bool rows;     // fork, one CTA: the rows of the table too
@@ -256,7 +257,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
       *a.status = status;
       if constexpr (MODE == kFork) ForkWs(a.ws, B).state[0] = status;
     }
-    if (status != 0) return;
+    if (status != 0) {
+      if (MODE == kExtend && rank == 0 && a.granted) // every CTA has read `in`
+#pragma unroll 1
+        for (int b = tid; b < B; b += kPlanThreads) a.granted[b] = 0;
+      return;
+    }
   } else if (rank == 0 && tid == 0) {
     *a.live = static_cast<int>(all);
     if (static_cast<int>(all) == pages) *CompactWs(a.ws, pages).moves = 0;
@@ -324,7 +330,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
   }
   if (MODE == kExtend && rank == 0) { // every CTA has read lens (first cluster barrier)
 #pragma unroll 1
-    for (int b = tid; b < B; b += kPlanThreads) a.p.lens[b] = max(a.p.lens[b], 0) + max(a.in[b], 0);
+    for (int b = tid; b < B; b += kPlanThreads) {
+      const int add = max(a.in[b], 0);
+      a.p.lens[b] = max(a.p.lens[b], 0) + add;
+      if (a.granted) a.granted[b] = add;
+    }
   }
 }
 
@@ -509,8 +519,8 @@ size_t pages_workspace_bytes(const tq_page_pool &p) {
   return (std::max(fork, compact) * sizeof(int) + 15) / 16 * 16;
 }
 
-cudaError_t launch_pages_extend(const tq_page_pool &p, const int *need, int *status, cudaStream_t s) {
-  return launch_plan(plan_kernel<kExtend>, s, PlanArgs{p, shift_of(p), need, status, nullptr, nullptr, false});
+cudaError_t launch_pages_extend(const tq_page_pool &p, const int *need, int *granted, int *status, cudaStream_t s) {
+  return launch_plan(plan_kernel<kExtend>, s, PlanArgs{p, shift_of(p), need, status, granted, nullptr, nullptr, false});
 }
 
 cudaError_t launch_pages_fork(const tq_page_pool &p, const tq_page_array *arrays, int n_arrays,
@@ -519,7 +529,7 @@ cudaError_t launch_pages_fork(const tq_page_pool &p, const tq_page_array *arrays
   // and its neighbours take 21.3 us instead of 23.6 us (host) and 12.5 instead of 13.0 us (GPU); with 96 x
   // 58 entries 25.7 us against 23.4 us over the whole GPU.
   const bool rows = p.num_pages <= kSmallPool && static_cast<long long>(p.B) * p.max_pages <= kSmallTable;
-  cudaError_t e = launch_plan(plan_kernel<kFork>, s, PlanArgs{p, shift_of(p), parent_of, status, nullptr, ws, rows});
+  cudaError_t e = launch_plan(plan_kernel<kFork>, s, PlanArgs{p, shift_of(p), parent_of, status, nullptr, nullptr, ws, rows});
   if (e != cudaSuccess || (rows && n_arrays == 0)) return e;
   if (!rows) {
     e = launch_pdl(fork_rows_kernel, row_grid(p), dim3(256), 0, s, p, shift_of(p), ws);
@@ -539,7 +549,7 @@ cudaError_t launch_pages_free(const tq_page_pool &p, const int *leaving, cudaStr
 
 cudaError_t launch_pages_compact(const tq_page_pool &p, const tq_page_array *arrays, int n_arrays, int *live,
                                  void *ws, int sm_count, cudaStream_t s) {
-  cudaError_t e = launch_plan(plan_kernel<kCompact>, s, PlanArgs{p, shift_of(p), nullptr, nullptr, live, ws, false});
+  cudaError_t e = launch_plan(plan_kernel<kCompact>, s, PlanArgs{p, shift_of(p), nullptr, nullptr, nullptr, live, ws, false});
   if (e != cudaSuccess) return e;
   return with_arrays(arrays, n_arrays, [&](const auto &ar) {
     using A = std::decay_t<decltype(ar)>;

@@ -228,7 +228,7 @@ constexpr int kMaxPoolB = 4096;       // sequences of a page pool
 constexpr int kMaxPageArrays = 1024;  // arrays (over all layers) that one call moves pages of
 constexpr int kPageCopyBatch = 256;   // (source, destination) pairs in one launch's parameters
 
-cudaError_t launch_pages_extend(const tq_page_pool &p, const int *need, int *status, cudaStream_t s);
+cudaError_t launch_pages_extend(const tq_page_pool &p, const int *need, int *granted, int *status, cudaStream_t s);
 cudaError_t launch_pages_fork(const tq_page_pool &p, const tq_page_array *arrays, int n_arrays,
                               const int *parent_of, int *status, void *ws, int sm_count, cudaStream_t s);
 cudaError_t launch_pages_free(const tq_page_pool &p, const int *leaving, cudaStream_t s);

@@ -147,6 +147,8 @@ EXPORTS = {
     "tq_pages_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(tq_page_pool)]),
     "tq_pages_extend": (ctypes.c_int, [ctypes.POINTER(tq_page_pool), ctypes.c_void_p, ctypes.c_void_p,
                                        ctypes.c_void_p]),
+    "tq_pages_extend_granted": (ctypes.c_int, [ctypes.POINTER(tq_page_pool), ctypes.c_void_p, ctypes.c_void_p,
+                                               ctypes.c_void_p, ctypes.c_void_p]),
     "tq_pages_fork": (ctypes.c_int, [ctypes.POINTER(tq_page_pool), ctypes.POINTER(tq_page_array), ctypes.c_int,
                                      ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
                                      ctypes.c_void_p]),
@@ -701,12 +703,19 @@ def _pool_arrays(pool: TQPagePool, arrays: TQPageArrays | None):
     return arrays.arrays, arrays.n
 
 
-def tq_pages_extend(pool: TQPagePool, need: torch.Tensor, status: torch.Tensor, stream=None) -> None:
+def tq_pages_extend(pool: TQPagePool, need: torch.Tensor, status: torch.Tensor, stream=None,
+                    granted: torch.Tensor | None = None) -> None:
     """lens[b] += need[b] (int32 [B]), with the lowest free pages. status (int32, one element): 0, or
     1 (not enough free pages) or 2 (a sequence would pass max_pages) and nothing changed. Pages behind a
-    length that the caller lowered (rejected drafts) go back first, in any case."""
-    _run(lib.tq_pages_extend, pool.device, stream, pool.ref, _i32(need, pool.B, "need", pool.device),
-         _i32(status, -1, "status", pool.device))
+    length that the caller lowered (rejected drafts) go back first, in any case. granted (int32 [B], need
+    itself allowed) gets the positions added, zeros where nothing changed: the counts of a step that
+    does not wait for the status on the host."""
+    dev = pool.device
+    np_, sp = _i32(need, pool.B, "need", dev), _i32(status, -1, "status", dev)
+    if granted is None:
+        _run(lib.tq_pages_extend, dev, stream, pool.ref, np_, sp)
+    else:
+        _run(lib.tq_pages_extend_granted, dev, stream, pool.ref, np_, _i32(granted, pool.B, "granted", dev), sp)
 
 
 def tq_pages_fork(pool: TQPagePool, arrays: TQPageArrays | None, parent_of: torch.Tensor, status: torch.Tensor,

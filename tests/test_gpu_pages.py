@@ -242,6 +242,87 @@ def test_bookkeeping_replays_from_a_graph():
         w.same()
 
 
+@pytest.mark.parametrize("B,max_pages,num_pages", [(3, 6, 9), (1500, 3, 2000), (12, 900, 20_000)])
+def test_granted_counts_are_what_was_added(B, max_pages, num_pages):
+    rng = np.random.default_rng(num_pages)
+    w = Both(B, max_pages, num_pages, 16, layers=0)
+    seen = set()
+    for step in range(8):
+        need = np.where(rng.random(B) < 0.7, rng.integers(-3, max_pages * 4, B), 0)
+        before = w.want.lens.copy()
+        asked, granted = _i32(need), _i32([99] * B)
+        tq.tq_pages_extend(w.pool, asked, w.status, granted=granted)
+        seen.add(w.want.extend(need))
+        w.same()
+        np.testing.assert_array_equal(granted.cpu().numpy(), w.want.lens - before)
+        assert torch.equal(asked.cpu(), torch.tensor(need, dtype=torch.int32))
+        if step % 3 == 2:
+            w.free(rng.random(B) < 0.5)
+    before = w.want.lens.copy()
+    asked = _i32([1] * B)  # the needs' own tensor takes the counts
+    tq.tq_pages_extend(w.pool, asked, w.status, granted=asked)
+    w.want.extend([1] * B)
+    np.testing.assert_array_equal(asked.cpu().numpy(), w.want.lens - before)
+    assert 0 in seen
+    granted = _i32([99] * B)  # more than a row of the table holds
+    tq.tq_pages_extend(w.pool, _i32([1] * (B - 1) + [max_pages * 16 + 1]), w.status, granted=granted)
+    assert int(w.status) == 2 and not granted.any()
+    w.same()
+    with pytest.raises(tq.TQError):
+        tq.tq_pages_extend(w.pool, asked, w.status, granted=asked[:1] if B > 1 else asked.long())
+
+
+def test_a_step_without_room_leaves_every_record_as_it_was():
+    """A captured step (extend, write, attend) whose sequences share pages: when pages run out it writes
+    nothing and attends to nothing, and goes on when there is room again."""
+    B, Hkv, d, page = 3, 2, 128, 16
+    pool = tq.TQPagePool(B, 6, 5, page)
+    cache = tq.TQMXCache(B, Hkv, d, page, 5, 6, pool.block_table)
+    arrays, ws_p = tq.tq_page_arrays(cache), tq.workspace(tq.tq_pages_workspace_bytes(pool))
+    need, n, status = _i32([32, 0, 0]), _i32([0] * B), _i32([7])
+    g = torch.Generator().manual_seed(8)
+    x = torch.randn(B, Hkv, 32, d, generator=g).to(torch.bfloat16).cuda()
+    q = torch.randn(B, 4, Hkv, d, generator=g).to(torch.bfloat16).cuda()
+    ws = tq.workspace(tq.tq_decode_mx_workspace_bytes(cache, Hkv, 4))
+    tq.tq_pages_extend(pool, need, status, granted=n)
+    tq.tq_quantize_kv_mx(x, x, cache, pool.lens, n)
+    tq.tq_pages_fork(pool, arrays, _i32([-1, 0, 0]), status, ws_p)  # all three share both pages
+    assert int(status) == 0 and int(pool.refs[0]) == 3
+    new = torch.randn(B, Hkv, 4, d, generator=g).to(torch.bfloat16).cuda()
+    out = torch.full_like(q, 5.0)
+
+    def step():
+        tq.tq_pages_extend(pool, need, status, granted=n)
+        tq.tq_quantize_kv_mx(new, new, cache, pool.lens, n)
+        tq.tq_decode_attention_mx(q, cache, pool.lens, d ** -0.5, out, ws, n)
+    need.copy_(_i32([0, 0, 0]))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    before = {k: t.clone() for k, t in cache.tensors.items()}
+    for ask, want in (([4, 17, 33], 1), ([4, 4, 100], 2)):  # six pages where three are free; a row too long
+        need.copy_(_i32(ask))
+        out.fill_(5.0)
+        graph.replay()
+        assert int(status) == want and pool.lens.tolist() == [32] * 3 and n.tolist() == [0] * 3
+        assert all(torch.equal(t, before[k]) for k, t in cache.tensors.items())
+        assert (out == 0).all()
+    need.copy_(_i32([4, 1, 3]))
+    graph.replay()
+    assert int(status) == 0 and n.tolist() == [4, 1, 3] and pool.lens.tolist() == [36, 33, 35]
+    for side in "kv":  # the shared pages are as they were
+        for p in pool.block_table[0, :2].tolist():
+            assert torch.equal(cache[f"{side}_codes"][p], before[f"{side}_codes"][p])
+    back = torch.empty_like(new)
+    tq.tq_dequantize_mx(cache, pool.lens, back, None, n)
+    assert (back[0] != 0).any(-1).all() and (back[1, :, 1:] == 0).all() and (out[2, :3] != 0).any(-1).all()
+
+
 # ------------------------------------------------------------------ together
 def test_a_serving_loop_of_two_layers():
     """Prompts arrive, steps are taken, one conversation is forked into samples, others leave, the pool

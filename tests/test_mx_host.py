@@ -225,3 +225,10 @@ def test_page_lists_of_any_integer_type():
         owner, address = tq._host_ints(x, "src")
         assert len(owner) == 2 and list((ctypes.c_int * 2).from_address(address)) == [3, 1]
     assert len(tq._host_ints([], "src")[0]) == 0 and len(tq._host_ints(np.array([], int), "src")[0]) == 0
+
+
+def test_extend_with_granted_counts_refuses_bad_arguments():
+    p, f = ctypes.byref(_pool()), tq.lib.tq_pages_extend_granted
+    assert f(None, P, P, P, None) == 1 and f(ctypes.byref(_pool(B=0)), P, P, P, None) == 1
+    assert f(p, None, P, P, None) == 1 and f(p, P, None, P, None) == 1 and f(p, P, P, None, None) == 1
+    assert f(p, P, P + 2, P, None) == 1 and "granted" in tq.last_error()
