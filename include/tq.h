@@ -328,14 +328,15 @@ typedef struct {
  * of a fused projection need no copy. Rows of no sequence, negative positions and positions past
  * max_pages * page_size or on unmapped pages are dropped; all other records stay as they were.
  * Two sequences must not write to one shared page (tq_pages_fork gives each its own).
- * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (d, dtype), TQ_ERR_CUDA. T = 0 is a no-op. */
+ * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (d, dtype), TQ_ERR_CUDA. T = 0 is a no-op (K and V may
+ * then both be NULL, as the address of an empty tensor is). */
 int tq_quantize_kv_mx(const void *K, const void *V, int dtype, int T, const int64_t *k_strides,
                       const int64_t *v_strides, const int32_t *lens, const int32_t *counts,
                       const tq_mx_cache *cache, void *stream);
 
 /* The counterpart: write the values of the same rows to K, V (contiguous [B][Hkv][T][d] of `dtype`,
  * device, either NULL). Rows that tq_quantize_kv_mx would drop read as zeros. With counts = lens
- * (and T >= every length) this is the whole sequence. */
+ * (and T >= every length) this is the whole sequence. T = 0 is a no-op. */
 int tq_dequantize_mx(const tq_mx_cache *cache, int T, const int32_t *lens, const int32_t *counts, void *K,
                      void *V, int dtype, void *stream);
 

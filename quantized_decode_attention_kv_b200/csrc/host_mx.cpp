@@ -90,7 +90,7 @@ int check_rows(const void *K, const void *V, int dtype, int T, const int32_t *le
   int st = check_mx(cache, &a->c);
   if (st) return st;
   if (!dtype_ok(dtype)) return fail(TQ_ERR_INVALID_ARG, "dtype=%d is not F32/BF16/F16", dtype);
-  if (!K && !V) return fail(TQ_ERR_INVALID_ARG, "K and V are both NULL");
+  if (!K && !V && T != 0) return fail(TQ_ERR_INVALID_ARG, "K and V are both NULL"); // without rows both may be
   if ((K && !aligned(K, 16)) || (V && !aligned(V, 16)))
     return fail(TQ_ERR_INVALID_ARG, "K/V pointers must be 16-byte aligned");
   if (T < 0 || T > (1 << 30)) return fail(TQ_ERR_INVALID_ARG, "T=%d must be in 0..2^30", T);

@@ -295,6 +295,21 @@ def test_write_and_read_leave_out_what_has_no_place():
                 assert (out[b, :, t] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", list(DT))
+def test_calls_of_no_rows_do_nothing(dtype):
+    cache = _cache(2, 2, 128, 16, 2)
+    _fill(cache, 0x5A)
+    x = torch.empty(2, 2, 0, 128, dtype=DT[dtype], device="cuda")
+    for K, V in ((x, x), (x, None), (None, x)):
+        for counts in (None, _i32([0, 0]), _i32([5, 0])):
+            tq.tq_quantize_kv_mx(K, V, cache, _i32([7, 0]), counts)
+            tq.tq_dequantize_mx(cache, _i32([7, 0]), K, V, counts)
+    torch.cuda.synchronize()
+    assert all((t == 0x5A).all() for t in cache.tensors.values())
+    with pytest.raises(tq.TQError):
+        tq.tq_quantize_kv_mx(None, None, cache, _i32([7, 0]))
+
+
 # ------------------------------------------------------------------ attention
 def _bound(att, d, T, out_dtype):
     """Largest admissible |error|, elementwise. Weights are fp16 (relative 2^-11; those below 2^-25 of

@@ -232,3 +232,13 @@ def test_extend_with_granted_counts_refuses_bad_arguments():
     assert f(None, P, P, P, None) == 1 and f(ctypes.byref(_pool(B=0)), P, P, P, None) == 1
     assert f(p, None, P, P, None) == 1 and f(p, P, None, P, None) == 1 and f(p, P, P, None, None) == 1
     assert f(p, P, P + 2, P, None) == 1 and "granted" in tq.last_error()
+
+
+def test_calls_of_no_rows_do_nothing():
+    # the address of a tensor without elements is NULL
+    c = ctypes.byref(_mx())
+    assert tq.lib.tq_quantize_kv_mx(None, None, 1, 0, None, None, P, None, c, None) == 0
+    assert tq.lib.tq_quantize_kv_mx(None, None, 1, 0, None, None, None, None, c, None) == 1  # lens is still checked
+    assert tq.lib.tq_dequantize_mx(c, 0, P, None, None, None, 1, None) == 0
+    assert tq.lib.tq_quantize_kv_mx(None, None, 1, 1, None, None, P, None, c, None) == 1
+    assert tq.lib.tq_dequantize_mx(c, 1, P, None, None, None, 1, None) == 1
