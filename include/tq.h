@@ -347,8 +347,9 @@ int tq_dequantize_mx(const tq_mx_cache *cache, int T, const int32_t *lens, const
  * a query that sees none, and rows of no sequence, give zeros. What a query does not see cannot
  * reach its output, NaN included. Where an infinity in a query makes all the scores it sees infinite, the
  * output is NaN, as their softmax is, for either sign. Sums and softmax in fp32; keys, values and queries enter the
- * tensor cores exactly (fp16 products of 6- and 11-bit significands), softmax weights in fp16.
- * Lq is 1..16, Hq a multiple of Hkv; the 16-position tiles of all sequences at full length, times KV
+ * tensor cores exactly (fp16 products of 6- and 11-bit significands), softmax weights in fp16: each is off
+ * by up to 2^-11 of itself, so an f32 output is good to about 2e-4 (relative L2), about what an fp16
+ * output holds. Lq is 1..16, Hq a multiple of Hkv; the 16-position tiles of all sequences at full length, times KV
  * heads and blocks of 8 rows (Lq Hq / Hkv), must stay below 2^32. The workspace depends on d only (not on the lengths, Hq or
  * Lq): one serves decode steps and drafts in turn; calls that may overlap on the GPU need one each. Errors: TQ_ERR_INVALID_ARG,
  * TQ_ERR_UNSUPPORTED, TQ_ERR_WORKSPACE, TQ_ERR_CUDA. */

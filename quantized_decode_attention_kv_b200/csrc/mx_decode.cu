@@ -27,10 +27,17 @@
 // 155 us; this way 25 us. Joining in the CTA that arrives last, in place of the combine kernel, saved
 // 2.4 us on the host and cost up to 9 us on the GPU, where one CTA had two long joins to do.)
 //
-// Bound: HBM by its bytes (144 a token and KV head at D = 128), instructions in practice. 16 x 32K
-// positions of 8 heads, D = 128, 4 query heads each: 604 MB in 119 us (5.1 TB/s, 78% of the copy rate;
-// the copies alone take 99 us), 275 warp instructions for 16 tokens, of which 64 conversions, 64
-// scalings and 17 MMAs. A step takes 32 tokens: with 16 it took 314 instructions and 126 us.
+// A sequence with fewer queries than the batch's widest (counts[b] < Lq) takes all row blocks all the same:
+// those without a query of it cost as much as the others and end as zeros. (Drafts of 0 to 5 queries at 4
+// query heads, blocks of 8 rows: 48% of the steps.)
+//
+// Bound: HBM by its bytes (144 a token and KV head at D = 128); in practice the latency of each warp's
+// chain of instructions. 16 x 32K positions of 8 heads, D = 128, 4 query heads each: 604 MB in 134 us over
+// rotating inputs (4.5 TB/s, 69% of the copy rate), 118 us in replays over one, where the copies alone
+// take 99. 273 warp instructions for 16 tokens, of which 64 conversions, 64 scalings and 17 MMAs, fill 58% of
+// the issue slots: registers leave a scheduler 3 warps, 1 of them ready on average, and they wait for fixed
+// latencies and busy pipes (2.3 of 4.8 cycles an instruction), hardly for memory (0.1). Heads of 64: 64% with
+// 4 warps. A step takes 32 tokens: with 16 it took 314 instructions and 126 us.
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
@@ -63,7 +70,7 @@ template <int D, int NT>
 struct Cfg {
   static constexpr int kCtas = D == 64 && NT == 1 ? 4 : D == 256 || (D == 128 && NT == 2) ? 2 : 3;
   static constexpr bool kQueriesInSmem = NT > 1;
-  static constexpr int kStages = D == 256 ? 2 : 3; // what fits
+  static constexpr int kStages = D == 256 ? 2 : 3; // what fits (D = 256, 8 warps: 16 x 16K positions, 604 MB, 113 us)
   static constexpr int kSixteen = 18 * D;            // bytes: 16 x (D/2 + D/16) of keys and of values
   static constexpr int kTile = kSub * kSixteen;
   static constexpr int kSlot = 8 * NT * (D + 2) * 4; // bytes of a partial: sums, then (reference, weight sum)
@@ -807,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) mx_decode_kernel(
           if (lane == 0) {
             const uint32_t last = s_bound[warp] + cu.at + cu.nt - 1; // the unit's last tile, in the whole space
             const int parts = static_cast<int>(min(split.share_of(last) / W, gridDim.x - 1u)) - cta + 1;
-          s_tail[warp] = make_int4(b, h, row0, max(parts, 1));
+            s_tail[warp] = make_int4(b, h, row0, max(parts, 1));
             s_rows[warp] = rows_of(k, b);
           }
         }

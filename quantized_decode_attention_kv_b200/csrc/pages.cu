@@ -10,8 +10,9 @@
 // entries ahead of the counts was no faster.)
 //
 // Bookkeeping of a call is one launch of one cluster: 1 CTA for pools of up to 16 K pages, 8 above
-// (a cluster costs a fork and its neighbours 3 us on the host and on the GPU for pools of 120 to 1300
-// pages; one CTA reads 16 K counts in four steps of its threads). Each warp counts its contiguous
+// (extend and free of 32 sequences, one CTA against 8: 7.4 and 8.8 us for 1000 pages, 8.2 and 9.6 for 4096,
+// 10.0 and 9.6 for 8192, 11.5 and 9.6 for 16384, 13.8 and 9.7 for 32768; compact 3.6 and 5.0, 4.5 and 6.0,
+// 5.9 and 6.6, 8.5 and 6.7, 13.4 and 6.6). Each warp counts its contiguous
 // share of the reference counts, the CTA totals are exchanged through distributed shared memory, and
 // a second look at the same counts (held as a bit mask a lane) hands out ranks. It is bound by
 // launch, memory latency and cold instructions, so its code is kept short. Page contents move as
@@ -525,9 +526,10 @@ cudaError_t launch_pages_extend(const tq_page_pool &p, const int *need, int *gra
 
 cudaError_t launch_pages_fork(const tq_page_pool &p, const tq_page_array *arrays, int n_arrays,
                               const int *parent_of, int *status, void *ws, int sm_count, cudaStream_t s) {
-  // One CTA also gathers and writes a small table's rows and saves a launch: with 5 x 19 entries a fork
-  // and its neighbours take 21.3 us instead of 23.6 us (host) and 12.5 instead of 13.0 us (GPU); with 96 x
-  // 58 entries 25.7 us against 23.4 us over the whole GPU.
+  // One CTA also gathers and writes a small table's rows and saves a launch, about 2 us of host time. GPU
+  // time of a fork so, and over the whole GPU (in brackets without arrays to copy): 8 x 16 entries 9.3
+  // against 9.8 (7.4, 9.8) us, 32 x 64 11.9 against 12.1 (9.5, 12.3), 64 x 64 14.2 against 13.5 (11.6, 13.4),
+  // 64 x 128 15.7 against 13.7 (13.0, 13.5). A row is one warp's: few long rows, 4 x 1024, take 19 against 11.
   const bool rows = p.num_pages <= kSmallPool && static_cast<long long>(p.B) * p.max_pages <= kSmallTable;
   cudaError_t e = launch_plan(plan_kernel<kFork>, s, PlanArgs{p, shift_of(p), parent_of, status, nullptr, nullptr, ws, rows});
   if (e != cudaSuccess || (rows && n_arrays == 0)) return e;
