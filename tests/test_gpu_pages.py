@@ -195,6 +195,22 @@ def test_a_page_that_goes_back_serves_the_same_call():
     w.same()
 
 
+def test_stepping_back_into_shared_pages_by_a_fork():
+    # below where it forked, a sequence shares the page it would go on in: forked at the lower length into
+    # an empty row it gets a copy of its own, and the row it leaves gives everything back
+    w = Both(4, 6, 20, 16, layers=1)
+    assert w.extend([40, 0, 0, 0]) == 0 and w.fork([-1, 0, -1, -1]) == 0
+    for lens in (w.pool.lens, w.want.lens):
+        lens[1] = 24  # in the second of two shared pages
+    assert w.fork([-1, -1, 1, -1]) == 0
+    w.free([0, 1, 0, 0])
+    w.same()
+    table = w.want.table
+    assert table[2, 0] == table[0, 0] and table[2, 1] != table[0, 1] and w.want.refs[table[2, 1]] == 1
+    assert w.extend([1, 0, 30, 0]) == 0
+    w.same()
+
+
 @pytest.mark.parametrize("n", [1, 5, 700])  # 700: more pairs than one launch carries
 def test_copy_moves_listed_pages_only(n):
     w = Both(1, 4, 1500, 16, layers=2, d=128, Hkv=3)
